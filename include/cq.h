@@ -49,6 +49,11 @@ extern "C" {
 #define CQ_MAX_E 8            /* environments supported */
 #define CQ_NUM_COUNTERS 8
 
+/* Element types of activations and gradients. */
+#define CQ_DTYPE_BF16 0
+#define CQ_DTYPE_FP16 1
+#define CQ_DTYPE_FP32 2
+
 typedef enum {
     CQ_OK = 0,
     CQ_ERR_INVALID_ARG = 1,      /* null pointer, bad size, layout or alignment */
@@ -219,6 +224,69 @@ cq_status cq_gptq_dequantize(const int32_t *qweight, const int32_t *qzeros, cons
                              const int32_t *g_idx, int64_t R, int64_t K, int out_fp16, void *out,
                              void *stream);
 
+/* ---- operators on the quantised weights -----------------------------------------
+ * A layer's weight is W[r][i] = scales[g][r] * (u[r][i] - (z[g][r] + 1)), g = i / 128, read
+ * from the v1 tensors above with act-order off: the operators do not take g_idx.
+ * A matrix operand [T][n] of 16-bit values has rows of n consecutive elements, ld
+ * elements apart: 16-byte aligned, ld % 8 == 0, ld >= n.  qweight is 16-byte aligned and
+ * scales 16-byte aligned.  dtype is CQ_DTYPE_BF16 or CQ_DTYPE_FP16.  T >= 0 rows (T == 0:
+ * nothing to do, except that summed gradients become zero); R % 8 == 0, K % 128 == 0, K > 0.
+ * Sums are fp32 (fp64 where stated) in a fixed order; every result is rounded once to its
+ * type.  Non-finite values propagate as IEEE arithmetic has them, within their own row of T
+ * (a product with a zero weight or zero input of the same row included). */
+#define CQ_ACT_NONE 0
+#define CQ_ACT_RELU 1      /* z < 0 ? 0 : z */
+#define CQ_ACT_GELU 2      /* z Phi(z), Phi the normal distribution function */
+#define CQ_ACT_GELU_TANH 3 /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+#define CQ_ACT_SILU 4      /* z / (1 + exp(-z)) */
+
+/* Linear layer: z = x W^T + bias, y = act(z) + residual.
+ *  x         [T][K], ldx.           bias      [R] of dtype, nullable.
+ *  residual  [T][R], ldres, nullable; may be y itself (with ldres == ldy).
+ *  y         [T][R], ldy.           pre       [T][R], ldpre, nullable: z, for the backward pass.
+ * x is multiplied by W; up to CQ_W4_EXACT_ROWS rows with W's exact values (integers in the
+ * products, the scale applied to each group's fp32 sum), above with W rounded to
+ * dtype to nearest even (as cq_gptq_dequantize's fp16 output; with fp16 a weight beyond
+ * 65504 is then infinite).  y and pre must not overlap x or each other. */
+#define CQ_W4_EXACT_ROWS 16
+cq_status cq_w4_linear(const void *x, int64_t ldx, int dtype, int64_t T, const int32_t *qweight,
+                       const int32_t *qzeros, const uint16_t *gptq_scales, int64_t R, int64_t K, const void *bias,
+                       int activation, const void *residual, int64_t ldres, void *y, int64_t ldy, void *pre,
+                       int64_t ldpre, void *stream);
+
+/* Its gradients, from dz [T][R] (lddz), the gradient at z:
+ *  dx       [T][K], lddx, nullable: dx = dz W, with W rounded to dtype as above.
+ *  dscales  fp32 [K/128][R], nullable: dscales[g][r] = sum_{i in g} (u - z - 1)[r][i] sum_t dz[t][r] x[t][i];
+ *           written, not added to.  x is read only for it (nullable otherwise).
+ * The gradient of the residual is the gradient of y itself; that of the bias comes from
+ * cq_activation_backward.  Outputs must not overlap inputs. */
+cq_status cq_w4_linear_backward(const void *dz, int64_t lddz, const void *x, int64_t ldx, int dtype, int64_t T,
+                                const int32_t *qweight, const int32_t *qzeros, const uint16_t *gptq_scales, int64_t R,
+                                int64_t K, void *dx, int64_t lddx, float *dscales, void *stream);
+
+/* dz = dy * act'(pre), rounded to dtype, and dbias[r] = sum_t of it before the rounding (fp32 [R], nullable,
+ * 4-byte aligned; written, not added to).  relu' is 1 where pre > 0, else 0; CQ_ACT_NONE copies dy.  All [T][R], R % 8 == 0; dz
+ * may be dy itself or pre itself (with the same ld). */
+cq_status cq_activation_backward(const void *dy, int64_t lddy, const void *pre, int64_t ldpre, int dtype, int64_t T,
+                                 int64_t R, int activation, void *dz, int64_t lddz, float *dbias, void *stream);
+
+/* Rows of a quantised table, from the selection's own scales [V*K/128] and codes [V*K/128][16] of a [V][K] matrix:
+ * out[t][i] = multiplier * (scale * q) of row ids[t], each product in fp32, rounded once to dtype (CQ_DTYPE_FP32 too);
+ * an id outside [0, V) gives a row of zeros.  ids are int32 (ids64 == 0) or int64 (ids64 == 1), out is [T][K]
+ * contiguous and 16-byte aligned, codes 4-byte aligned. */
+cq_status cq_w4_embedding(const void *ids, int ids64, int64_t T, const uint16_t *scales, const uint32_t *codes,
+                          int64_t V, int64_t K, float multiplier, int dtype, void *out, void *stream);
+
+/* Gradient of that table's scales from dout [T][K] (contiguous, 16-byte aligned, dtype as above):
+ *   dscales[v][g] = multiplier * sum_{t: ids[t] = v} sum_{i in g} dout[t][i] q[v][i]    fp32 [V][K/128]
+ * written whole (zero for a row that no id names).  The tokens are sorted by id (stable), the sums over a
+ * row's tokens taken in fp64 in a fixed order.  workspace: device, 256-byte aligned, at least
+ * cq_w4_embedding_backward_workspace_bytes(T, K); calls that share one must be ordered on one stream. T < 2^31. */
+size_t cq_w4_embedding_backward_workspace_bytes(int64_t T, int64_t K);
+cq_status cq_w4_embedding_backward(const void *dout, int dtype, const void *ids, int ids64, int64_t T,
+                                   const uint32_t *codes, int64_t V, int64_t K, float multiplier, float *dscales,
+                                   void *workspace, size_t workspace_bytes, void *stream);
+
 /* ---- sensitivity diagonals ----------------------------------------------------
  * The project page ("What CliffQuant changes"; "The negative result that
  * changed the method") takes separately normalised per-environment diagonals
@@ -231,9 +299,6 @@ cq_status cq_gptq_dequantize(const int32_t *qweight, const int32_t *qzeros, cons
  * Squares are exact and summed in fp64 in a fixed order (deterministic).  An
  * environment with no rows, or only zero activations, gives NaN.  D is the
  * per-column diagonal layout cq_select_scales takes. */
-#define CQ_DTYPE_BF16 0
-#define CQ_DTYPE_FP16 1
-#define CQ_DTYPE_FP32 2
 cq_status cq_estimate_diagonals(const void *X, int dtype, int64_t K, const int64_t *row_offsets, int E,
                                 double *means, float *D, void *stream);
 

@@ -28,7 +28,9 @@ MAX_E = 8
 # Symbols the C header declares, in declaration order.
 EXPORTS = ("cq_workspace_bytes", "cq_select_scales", "cq_select_scales_ex", "cq_select_scales_host",
            "cq_absmax_scales", "cq_pool_diagonals", "cq_group_objective", "cq_reconstruction_proxy",
-           "cq_gptq_export", "cq_gptq_dequantize", "cq_estimate_diagonals", "cq_select_scales_spec",
+           "cq_gptq_export", "cq_gptq_dequantize", "cq_w4_linear", "cq_w4_linear_backward",
+           "cq_activation_backward", "cq_w4_embedding", "cq_w4_embedding_backward_workspace_bytes",
+           "cq_w4_embedding_backward", "cq_estimate_diagonals", "cq_select_scales_spec",
            "cq_select_scales_noalloc", "cq_trim_memory", "cq_read_counters", "cq_get_status", "cq_status_string",
            "cq_version")
 
@@ -80,6 +82,19 @@ def _load():
     L.cq_gptq_export.argtypes = [vp, vp, i64, i64, vp, vp, vp, vp, vp]
     L.cq_gptq_dequantize.restype = i32
     L.cq_gptq_dequantize.argtypes = [vp, vp, vp, vp, i64, i64, i32, vp, vp]
+    L.cq_w4_linear.restype = i32
+    L.cq_w4_linear.argtypes = [vp, i64, i32, i64, vp, vp, vp, i64, i64, vp, i32, vp, i64, vp, i64, vp, i64, vp]
+    L.cq_w4_linear_backward.restype = i32
+    L.cq_w4_linear_backward.argtypes = [vp, i64, vp, i64, i32, i64, vp, vp, vp, i64, i64, vp, i64, vp, vp]
+    L.cq_activation_backward.restype = i32
+    L.cq_activation_backward.argtypes = [vp, i64, vp, i64, i32, i64, i64, i32, vp, i64, vp, vp]
+    L.cq_w4_embedding.restype = i32
+    L.cq_w4_embedding.argtypes = [vp, i32, i64, vp, vp, i64, i64, ctypes.c_float, i32, vp, vp]
+    L.cq_w4_embedding_backward_workspace_bytes.restype = ctypes.c_size_t
+    L.cq_w4_embedding_backward_workspace_bytes.argtypes = [i64, i64]
+    L.cq_w4_embedding_backward.restype = i32
+    L.cq_w4_embedding_backward.argtypes = [vp, i32, vp, i32, i64, vp, i64, i64, ctypes.c_float, vp, vp,
+                                           ctypes.c_size_t, vp]
     L.cq_estimate_diagonals.restype = i32
     L.cq_estimate_diagonals.argtypes = [vp, i32, i64, vp, i32, vp, vp, vp]
     L.cq_select_scales_spec.restype = i32
@@ -489,6 +504,268 @@ def estimate_diagonals(X, row_offsets, *, dtype=None, stream=None, means=None, o
     _check(lib.cq_estimate_diagonals(_ptr(X), int(dtype), K, _ptr(off), E, _ptr(means), _ptr(out),
                                      _stream_handle(stream)), "cq_estimate_diagonals")
     return means, out
+
+
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+
+
+@dataclass
+class W4Weights:
+    """GPTQ v1 tensors of one linear layer that w4_weights has checked, for the
+    operators below (act-order off: input i is in group i // 128)."""
+    qweight: "object"  # torch.int32 [K/8, R]
+    qzeros: "object"   # torch.int32 [K/128, R/8]
+    scales: "object"   # torch.float16 [K/128, R]
+    R: int
+    K: int
+
+
+def w4_weights(t: GPTQTensors) -> W4Weights:
+    """Checks GPTQ v1 tensors once, for w4_linear and w4_linear_backward: shapes,
+    types, devices, and that g_idx is i // 128 (read to the host here; an
+    act-order layer raises ValueError)."""
+    import torch
+    if t.qweight.dim() != 2:
+        raise ValueError("qweight must be [K/8, R]")
+    K, R = t.qweight.shape[0] * 8, t.qweight.shape[1]
+    if K % GROUP or K == 0 or R % 8:
+        raise ValueError("K must be a positive multiple of 128 and R a multiple of 8")
+    for name, v, shape, dtype in (("qweight", t.qweight, (K // 8, R), torch.int32),
+                                  ("qzeros", t.qzeros, (K // GROUP, R // 8), torch.int32),
+                                  ("scales", t.scales, (K // GROUP, R), torch.float16),
+                                  ("g_idx", t.g_idx, (K,), torch.int32)):
+        if tuple(v.shape) != shape or v.dtype != dtype or not v.is_contiguous():
+            raise ValueError(f"{name} must be contiguous {dtype} {list(shape)}")
+    if not all(v.is_cuda and v.device == t.qweight.device for v in (t.qweight, t.qzeros, t.scales, t.g_idx)):
+        raise ValueError("the tensors must be CUDA tensors of one device")
+    if not np.array_equal(t.g_idx.cpu().numpy(), np.arange(K) // GROUP):
+        raise ValueError("g_idx must be i // 128: act-order layers are not supported here")
+    return W4Weights(t.qweight, t.qzeros, t.scales, R, K)
+
+
+class _On:
+    """Device and stream of one call: `dev` current, outputs allocated on `stream`."""
+
+    def __init__(self, dev, stream):
+        import torch
+        if stream is not None and stream.device != dev:
+            raise ValueError("stream belongs to another device than the tensors")
+        self.stream = torch.cuda.current_stream(dev) if stream is None else stream
+        self.context = None
+        if stream is not None or dev.index != torch.cuda.current_device():
+            self.context = torch.cuda.stream(self.stream)
+
+    def __enter__(self):
+        if self.context is not None:
+            self.context.__enter__()
+        return ctypes.c_void_p(self.stream.cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.context is not None:
+            self.context.__exit__(*exc)
+        return False
+
+
+def _rows16(name, t, rows, cols, like):
+    """Checks a [rows, cols] operand whose rows may be strided; returns its row stride."""
+    if tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
+    if t.dtype != like.dtype or t.device != like.device:
+        raise ValueError(f"{name} must be {like.dtype} on {like.device}")
+    if rows == 0 or cols == 0:
+        return cols
+    ld = t.stride(0) if rows > 1 else max(t.stride(0), cols)
+    if rows == 1 and ld % 8:
+        ld = cols
+    if (cols > 1 and t.stride(1) != 1) or ld < cols or ld % 8 or t.data_ptr() % 16:
+        raise ValueError(f"{name} must have contiguous rows that start on 16-byte boundaries")
+    return ld
+
+
+def _dtype16(name, t):
+    import torch
+    if not t.is_cuda or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D CUDA tensor")
+    if t.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"{name} must be bfloat16 or float16")
+    return DTYPE_BF16 if t.dtype == torch.bfloat16 else DTYPE_FP16
+
+
+def _activation(activation):
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"unknown activation {activation!r}; expected one of {tuple(ACTIVATIONS)}")
+    return ACTIVATIONS[activation]
+
+
+def _check_same_device(w, t):
+    if w.qweight.device != t.device:
+        raise ValueError("the weights are on another device than the activations")
+
+
+def w4_linear(x, w: W4Weights, *, bias=None, activation: str = "none", residual=None, want_pre: bool = False,
+              stream=None, out=None, pre=None):
+    """y = activation(x W^T + bias) + residual, W the layer's 4-bit weights.
+
+    x: [T, K] bfloat16 or float16, rows contiguous (they may be strided) and
+       16-byte aligned; bias [R], residual [T, R] of x's type.  ``out`` may be
+       the residual itself.  activation: one of ACTIVATIONS.
+       Returns y [T, R], or (y, pre) with ``want_pre``: pre = x W^T + bias, which
+       activation_backward takes."""
+    import torch
+    dt, act = _dtype16("x", x), _activation(activation)
+    _check_same_device(w, x)
+    T, R, K = x.shape[0], w.R, w.K
+    ldx = _rows16("x", x, T, K, x)
+    if bias is not None and (tuple(bias.shape) != (R,) or bias.dtype != x.dtype or bias.device != x.device or
+                             not bias.is_contiguous()):
+        raise ValueError(f"bias must be a contiguous {x.dtype} [{R}] tensor on {x.device}")
+    ldres = _rows16("residual", residual, T, R, x) if residual is not None else 0
+    with _On(x.device, stream) as handle:
+        if out is None:
+            out = torch.empty((T, R), dtype=x.dtype, device=x.device)
+        if want_pre and pre is None:
+            pre = torch.empty((T, R), dtype=x.dtype, device=x.device)
+        ldy = _rows16("out", out, T, R, x)
+        ldpre = _rows16("pre", pre, T, R, x) if pre is not None else 0
+        _check(lib.cq_w4_linear(_ptr(x), ldx, dt, T, _ptr(w.qweight), _ptr(w.qzeros), _ptr(w.scales), R, K, _ptr(bias),
+                                act, _ptr(residual), ldres, _ptr(out), ldy, _ptr(pre), ldpre, handle), "cq_w4_linear")
+    return (out, pre) if want_pre else out
+
+
+def w4_linear_backward(dz, x, w: W4Weights, *, want_dx: bool = True, want_dscales: bool = True, stream=None,
+                       dx=None, dscales=None):
+    """Gradients of x W^T at dz [T, R]: (dx [T, K] of dz's type, dscales float32
+    [K/128, R], the gradient of the layer's group scales); None in the place of
+    one that is not wanted (x is read only for dscales)."""
+    import torch
+    dt = _dtype16("dz", dz)
+    _check_same_device(w, dz)
+    T, R, K = dz.shape[0], w.R, w.K
+    lddz = _rows16("dz", dz, T, R, dz)
+    ldx = _rows16("x", x, T, K, dz) if want_dscales else 0
+    if dscales is not None and (tuple(dscales.shape) != (K // GROUP, R) or dscales.dtype != torch.float32 or
+                                dscales.device != dz.device or not dscales.is_contiguous()):
+        raise ValueError(f"dscales must be contiguous float32 [{K // GROUP}, {R}]")
+    with _On(dz.device, stream) as handle:
+        if want_dx and dx is None:
+            dx = torch.empty((T, K), dtype=dz.dtype, device=dz.device)
+        if want_dscales and dscales is None:
+            dscales = torch.empty((K // GROUP, R), dtype=torch.float32, device=dz.device)
+        if not want_dx:
+            dx = None
+        if not want_dscales:
+            x = dscales = None
+        lddx = _rows16("dx", dx, T, K, dz) if dx is not None else 0
+        _check(lib.cq_w4_linear_backward(_ptr(dz), lddz, _ptr(x), ldx, dt, T, _ptr(w.qweight), _ptr(w.qzeros),
+                                         _ptr(w.scales), R, K, _ptr(dx), lddx, _ptr(dscales), handle),
+               "cq_w4_linear_backward")
+    return dx, dscales
+
+
+def activation_backward(dy, pre, activation: str, *, want_dbias: bool = True, stream=None, out=None, dbias=None):
+    """(dz, dbias) from the gradient dy at act(pre) + residual: dz = dy act'(pre) in
+    dy's type, dbias its column sums (float32 [R], taken before that rounding)
+    or None.  dy, pre: [T, R] bfloat16 or float16; R a multiple of 8."""
+    import torch
+    dt, act = _dtype16("dy", dy), _activation(activation)
+    T, R = dy.shape
+    if R % 8:
+        raise ValueError("R must be a multiple of 8")
+    lddy, ldpre = _rows16("dy", dy, T, R, dy), _rows16("pre", pre, T, R, dy)
+    if dbias is not None and (tuple(dbias.shape) != (R,) or dbias.dtype != torch.float32 or dbias.device != dy.device or
+                              not dbias.is_contiguous()):
+        raise ValueError(f"dbias must be contiguous float32 [{R}]")
+    with _On(dy.device, stream) as handle:
+        if out is None:
+            out = torch.empty((T, R), dtype=dy.dtype, device=dy.device)
+        if want_dbias and dbias is None:
+            dbias = torch.empty(R, dtype=torch.float32, device=dy.device)
+        if not want_dbias:
+            dbias = None
+        lddz = _rows16("out", out, T, R, dy)
+        _check(lib.cq_activation_backward(_ptr(dy), lddy, _ptr(pre), ldpre, dt, T, R, act, _ptr(out), lddz, _ptr(dbias),
+                                          handle), "cq_activation_backward")
+    return out, dbias
+
+
+def _table(ids, codes, K):
+    """(tokens, rows) of a lookup of ids in a quantised table of K columns."""
+    import torch
+    if not ids.is_cuda or ids.dtype not in (torch.int32, torch.int64) or not ids.is_contiguous():
+        raise ValueError("ids must be a contiguous CUDA int32 or int64 tensor")
+    if K <= 0 or K % GROUP:
+        raise ValueError("K must be a positive multiple of 128")
+    if codes.element_size() != 4 or codes.device != ids.device or not codes.is_contiguous() or codes.numel() % (K // 8):
+        raise ValueError("codes must hold contiguous 32-bit words of whole rows, on the device of ids")
+    return ids.numel(), codes.numel() // (K // 8)
+
+
+def w4_embedding(ids, scales, codes, K: int, *, multiplier: float = 1.0, dtype=None, stream=None, out=None):
+    """Rows ids of a [V, K] table quantised by select_scales (scales [V*K/128],
+    codes [V*K/128, 16]): multiplier * scale * q, rounded once to ``dtype`` (float16
+    by default, bfloat16 or float32).  An id outside [0, V) gives zeros.
+    ids: int32 or int64 of any shape; returns [*ids.shape, K]."""
+    import torch
+    K = int(K)
+    T, V = _table(ids, codes, K)
+    if scales.element_size() != 2 or scales.numel() != V * (K // GROUP) or scales.device != ids.device or \
+            not scales.is_contiguous():
+        raise ValueError("scales must hold V*K/128 contiguous 16-bit patterns on the device of ids")
+    if out is not None:
+        dtype = out.dtype if dtype is None else dtype
+    dtype = torch.float16 if dtype is None else dtype
+    dt = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_FP16, torch.float32: DTYPE_FP32}.get(dtype)
+    if dt is None:
+        raise ValueError("dtype must be bfloat16, float16 or float32")
+    shape = tuple(ids.shape) + (K,)
+    if out is not None and (tuple(out.shape) != shape or out.dtype != dtype or out.device != ids.device or
+                            not out.is_contiguous()):
+        raise ValueError(f"out must be contiguous {dtype} {list(shape)}")
+    with _On(ids.device, stream) as handle:
+        if out is None:
+            out = torch.empty(shape, dtype=dtype, device=ids.device)
+        _check(lib.cq_w4_embedding(_ptr(ids), int(ids.dtype == torch.int64), T, _ptr(scales), _ptr(codes), V, K,
+                                   float(multiplier), dt, _ptr(out), handle), "cq_w4_embedding")
+    return out
+
+
+def w4_embedding_workspace_bytes(T: int, K: int) -> int:
+    return int(lib.cq_w4_embedding_backward_workspace_bytes(int(T), int(K)))
+
+
+def w4_embedding_backward(dout, ids, codes, *, multiplier: float = 1.0, stream=None, out=None, workspace=None):
+    """Gradient of a quantised table's group scales: float32 [V, K/128], zero for
+    the rows that no id names.  dout: [*ids.shape, K] bfloat16, float16 or
+    float32; ids outside [0, V) have no gradient.  ``workspace``: uint8, at least
+    w4_embedding_workspace_bytes(T, K); calls that share one must be ordered on
+    one stream."""
+    import torch
+    if not dout.is_cuda or dout.dim() < 1 or not dout.is_contiguous() or tuple(dout.shape[:-1]) != tuple(ids.shape):
+        raise ValueError("dout must be a contiguous CUDA tensor [*ids.shape, K]")
+    dt = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_FP16, torch.float32: DTYPE_FP32}.get(dout.dtype)
+    if dt is None:
+        raise ValueError("dout must be bfloat16, float16 or float32")
+    K = dout.shape[-1]
+    T, V = _table(ids, codes, K)
+    if dout.device != ids.device:
+        raise ValueError("dout must be on the device of ids")
+    if out is not None and (tuple(out.shape) != (V, K // GROUP) or out.dtype != torch.float32 or
+                            out.device != ids.device or not out.is_contiguous()):
+        raise ValueError(f"out must be contiguous float32 [{V}, {K // GROUP}]")
+    wsb = w4_embedding_workspace_bytes(T, K)
+    if workspace is not None and (workspace.device != ids.device or not workspace.is_contiguous() or
+                                  workspace.numel() * workspace.element_size() < wsb):
+        raise ValueError(f"workspace must hold {wsb} contiguous bytes on the device of ids")
+    with _On(ids.device, stream) as handle:
+        if out is None:
+            out = torch.empty((V, K // GROUP), dtype=torch.float32, device=ids.device)
+        if workspace is None:
+            workspace = torch.empty(wsb, dtype=torch.uint8, device=ids.device)
+        _check(lib.cq_w4_embedding_backward(_ptr(dout), dt, _ptr(ids), int(ids.dtype == torch.int64), T, _ptr(codes), V, K,
+                                            float(multiplier), _ptr(out), _ptr(workspace), wsb, handle),
+               "cq_w4_embedding_backward")
+    return out
+
 
 
 def read_counters(workspace, stream=None) -> dict:
