@@ -46,9 +46,11 @@ template <int N>
 struct Stages {
     static constexpr int kB = N * kChunk * 2;
     static constexpr int kOperands = N >= 256 ? 4 : 5;
-    static constexpr int kRaw = N >= 256 ? 3 : N >= 128 ? 6 : 10;
+    static constexpr int kRaw = N >= 256 ? 2 : N >= 128 ? 5 : 10;
     static constexpr int kBarriers = 2 * kOperands + 2 * kRaw + 4;
-    static constexpr int kBytes = kOperands * (kAStage + kB) + kRaw * kRawStage + 8 * kBarriers + 16 + 1024;
+    static constexpr int kControl = 8 * kBarriers + 16;      // barriers, the stop flag, tensor memory's address
+    static constexpr int kTurn = 4 * 16 * 33 * 4;            // the epilogue's turn from lanes to rows
+    static constexpr int kBytes = kOperands * (kAStage + kB) + kRaw * kRawStage + kControl + kTurn + 1024;
     static constexpr int kColumns = 2 * N < 32 ? 32 : 2 * N;
     static_assert(kBytes <= 232448, "shared memory");
 };
@@ -125,6 +127,24 @@ struct Epilogue {
     int act;
 };
 
+template <class D>
+__device__ __forceinline__ void widen(const uint4 &u, float (&v)[8])
+{
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        v[2 * j] = D::to_float(static_cast<uint16_t>(w[j]));
+        v[2 * j + 1] = D::to_float(static_cast<uint16_t>(w[j] >> 16));
+    }
+}
+
+template <class D>
+__device__ __forceinline__ uint4 narrow(const float (&v)[8])
+{
+    return make_uint4(D::from_floats(v[0], v[1]), D::from_floats(v[2], v[3]), D::from_floats(v[4], v[5]),
+                      D::from_floats(v[6], v[7]));
+}
+
 // A ring's slot and the parity of its phase.
 template <int kSlots>
 struct Ring {
@@ -190,38 +210,55 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
     tc::fence_after();
     const uint32_t tmem = *tmem_at;
 
-    if (warp < 4) {  // epilogue: a thread has one m, a chunk of 32 tokens at a time
+    if (warp < 4) {
+        // Epilogue, a warp's 32 m by 16 tokens at a time: a thread has one m in tensor memory;
+        // through 2 KB of shared memory it gets 8 adjacent m of one token, 16 bytes of every row it touches.
+        float *turn = reinterpret_cast<float *>(shared + (bars - base) + S::kControl) + warp * (16 * 33);
         Ring<2> sums;
+        const int tok = lane >> 2, part = 8 * (lane & 3);
         for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-            const int64_t m = tile / tiles_n * kM + 32 * warp + lane, t0 = tile % tiles_n * N;
-            const float bias = ep.bias && m < rows ? D::to_float(ep.bias[m]) : 0.0f;
+            const int64_t m0 = tile / tiles_n * kM + 32 * warp, t0 = tile % tiles_n * N, m = m0 + part;
+            const float bias = ep.bias && m0 + lane < rows ? D::to_float(ep.bias[m0 + lane]) : 0.0f;
+            const int64_t left = T - t0;
+            const int tokens = left < N ? static_cast<int>(left) : N;
             if (!tc::barrier_wait_warp(sums_full(sums.slot), sums.parity, stop))
                 break;
             tc::fence_after();
-            for (int c = 0; c < N; c += 32) {
-                if (t0 + c >= T)
-                    break;
-                uint32_t v[32];
-                __syncwarp();
-                tc::tmem_load32(tmem + (static_cast<uint32_t>(32 * warp) << 16) + sums.slot * N + c, v);
-                if (m < rows) {
+            for (int c = 0; c < tokens; c += 16) {
+                uint4 res[2];
 #pragma unroll
-                    for (int j = 0; j < 32; j++) {
-                        const int64_t t = t0 + c + j;
-                        if (t >= T)
-                            break;
-                        const float z = __uint_as_float(v[j]) + bias;
-                        if (kGradient) {
-                            ep.y[t * ep.ldy + m] = D::from_float(z);
-                            continue;
-                        }
+                for (int h = 0; h < 2; h++)
+                    if (!kGradient && ep.res && m < rows && c + 8 * h + tok < tokens)
+                        res[h] = *reinterpret_cast<const uint4 *>(ep.res + (t0 + c + 8 * h + tok) * ep.ldres + m);
+                uint32_t v[16];
+                tc::tmem_load16(tmem + (static_cast<uint32_t>(32 * warp) << 16) + sums.slot * N + c, v);
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 16; j++)
+                    turn[j * 33 + lane] = __uint_as_float(v[j]) + bias;
+                __syncwarp();
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    if (m >= rows || c + 8 * h + tok >= tokens)  // rows % 8 == 0: eight m in or out together
+                        continue;
+                    const int64_t t = t0 + c + 8 * h + tok;
+                    float z[8];
+#pragma unroll
+                    for (int j = 0; j < 8; j++)
+                        z[j] = turn[(8 * h + tok) * 33 + part + j];
+                    if (!kGradient) {
                         if (ep.pre)
-                            ep.pre[t * ep.ldpre + m] = D::from_float(z);
-                        float o = activate(z, ep.act);
-                        if (ep.res)
-                            o += D::to_float(ep.res[t * ep.ldres + m]);
-                        ep.y[t * ep.ldy + m] = D::from_float(o);
+                            *reinterpret_cast<uint4 *>(ep.pre + t * ep.ldpre + m) = narrow<D>(z);
+                        activate(z, ep.act);
+                        if (ep.res) {
+                            float r[8];
+                            widen<D>(res[h], r);
+#pragma unroll
+                            for (int j = 0; j < 8; j++)
+                                z[j] += r[j];
+                        }
                     }
+                    *reinterpret_cast<uint4 *>(ep.y + t * ep.ldy + m) = narrow<D>(z);
                 }
             }
             tc::fence_before();
@@ -356,17 +393,192 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
         tc::tmem_free(tmem, S::kColumns);
 }
 
+// ---- few rows ----------------------------------------------------------------------------------
+//
+// Up to 16 rows the weights' bytes are the work: a CTA has 32 outputs, its 8 warps (of all
+// the CTAs of a cluster) take the groups in turn.  A thread loads 4 outputs' words at once (16 bytes,
+// 4 lanes of a word row make 128-byte runs over 8 lanes); a word is 8 inputs, whose pairs (q, q + 4)
+// come out of it with a shift and a mask.  That order of the inputs is as good as any for the
+// m16n8k16 product if the activations' pairs are the same.  The codes enter as integers and each
+// group's fp32 sum is scaled after, so the weights are exact.
+// The warps' and the cluster's sums meet in shared memory in a fixed order.
+
+constexpr int kFewWarps = 8;
+constexpr int kFewRows = 32;   // outputs per CTA
+
+template <class D>
+__device__ __forceinline__ void mma_16x8x16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
+
+template <>
+__device__ __forceinline__ void mma_16x8x16<BF16>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <>
+__device__ __forceinline__ void mma_16x8x16<FP16>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// What a thread needs of one group: 4 word rows of its 4 outputs, their scales and
+// zero points, and 32 inputs of one token of each tile of 8.
+template <int NT>
+struct GroupData {
+    uint4 words[4];
+    uint2 scales;
+    uint32_t zeros;
+    uint4 x[NT][4];
+};
+
+template <class D, int NT>
+__global__ void __launch_bounds__(32 * kFewWarps)
+    few_rows_kernel(const uint16_t *__restrict__ x, int64_t ldx, int T, Layer w, Epilogue ep)
+{
+    __shared__ float sums[kFewWarps][8 * NT * kFewRows];
+    __shared__ float cta_sums[8 * NT * kFewRows];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int ranks = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int quad = lane >> 2, c = lane & 3;
+    const int64_t r0 = static_cast<int64_t>(blockIdx.x / ranks) * kFewRows, r = r0 + 4 * quad;
+    const bool inside = r < w.R;  // R % 8 == 0: four outputs in or out together
+    const int64_t groups = w.K / kGroup;
+
+    auto load = [&](int64_t g, GroupData<NT> &d) {
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            d.words[j] = inside ? __ldcs(reinterpret_cast<const uint4 *>(w.qweight + (g * kWordsPerGroup + 4 * j + c) * w.R + r))
+                                : make_uint4(0, 0, 0, 0);
+        d.scales = inside ? *reinterpret_cast<const uint2 *>(w.scales + g * w.R + r) : make_uint2(0, 0);
+        d.zeros = inside ? w.qzeros[(g * w.R + r) / 8] >> (4 * (r & 7)) : 0u;
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                d.x[n][j] = 8 * n + quad < T
+                                ? *reinterpret_cast<const uint4 *>(x + (8 * n + quad) * ldx + g * kGroup + 8 * (4 * j + c))
+                                : make_uint4(0, 0, 0, 0);
+    };
+
+    float total[2][NT][4] = {};
+    auto multiply = [&](const GroupData<NT> &d) {
+        float acc[2][NT][4] = {};
+        uint32_t zero[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            zero[i] = zero_pair<D>((d.zeros >> (4 * i)) & 15u);
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const uint32_t word[4] = {d.words[j].x, d.words[j].y, d.words[j].z, d.words[j].w};
+            uint32_t pair[4][4];  // [output][q]: inputs q and q + 4
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+#pragma unroll
+                for (int q = 0; q < 4; q++)
+                    pair[i][q] = D::sub(((word[i] >> (4 * q)) & 0x000F000Fu) | D::kMagic, zero[i]);
+#pragma unroll
+            for (int n = 0; n < NT; n++) {
+                const uint4 v = d.x[n][j];
+                const uint32_t b[4] = {__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                                       __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632)};
+#pragma unroll
+                for (int p = 0; p < 2; p++) {
+#pragma unroll
+                    for (int s = 0; s < 2; s++) {
+                        const uint32_t a[4] = {pair[2 * p][2 * s], pair[2 * p + 1][2 * s], pair[2 * p][2 * s + 1],
+                                               pair[2 * p + 1][2 * s + 1]};
+                        mma_16x8x16<D>(acc[p][n], a, b[2 * s], b[2 * s + 1]);
+                    }
+                }
+            }
+        }
+        const float s[4] = {half_bits(static_cast<uint16_t>(d.scales.x)), half_bits(static_cast<uint16_t>(d.scales.x >> 16)),
+                            half_bits(static_cast<uint16_t>(d.scales.y)), half_bits(static_cast<uint16_t>(d.scales.y >> 16))};
+#pragma unroll
+        for (int p = 0; p < 2; p++)
+#pragma unroll
+            for (int n = 0; n < NT; n++)
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    total[p][n][i] = fmaf(s[2 * p + (i >> 1)], acc[p][n][i], total[p][n][i]);
+    };
+
+    const int64_t step = static_cast<int64_t>(ranks) * kFewWarps;
+    int64_t g = static_cast<int64_t>(rank) * kFewWarps + warp;
+    if (g < groups) {
+        GroupData<NT> now, next;
+        load(g, now);
+        for (; g < groups; g += step) {
+            if (g + step < groups)
+                load(g + step, next);
+            multiply(now);
+            now = next;
+        }
+    }
+#pragma unroll
+    for (int p = 0; p < 2; p++)
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                sums[warp][(8 * n + 2 * c + (i & 1)) * kFewRows + 4 * quad + 2 * p + (i >> 1)] = total[p][n][i];
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < NT; n++) {
+        const int e = threadIdx.x + n * 32 * kFewWarps;
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kFewWarps; i++)
+            s += sums[i][e];
+        cta_sums[e] = s;
+    }
+    if (ranks > 1)
+        cluster.sync();
+    else
+        __syncthreads();
+    const int share = 8 * NT * kFewRows / ranks;
+    if (static_cast<int>(threadIdx.x) < share || NT > 1) {
+        for (int i = threadIdx.x; i < share; i += 32 * kFewWarps) {
+            const int e = rank * share + i, t = e / kFewRows;
+            const int64_t out = r0 + e % kFewRows;
+            float z[1] = {0.0f};
+            for (int k = 0; k < ranks; k++)
+                z[0] += ranks > 1 ? cluster.map_shared_rank(cta_sums, k)[e] : cta_sums[e];
+            if (t >= T || out >= w.R)
+                continue;
+            z[0] += ep.bias ? D::to_float(ep.bias[out]) : 0.0f;
+            if (ep.pre)
+                ep.pre[t * ep.ldpre + out] = D::from_float(z[0]);
+            activate(z, ep.act);
+            if (ep.res)
+                z[0] += D::to_float(ep.res[t * ep.ldres + out]);
+            ep.y[t * ep.ldy + out] = D::from_float(z[0]);
+        }
+    }
+    if (ranks > 1)
+        cluster.sync();  // peers keep their shared memory until it has been read
+}
+
 // ---- scale gradient ----------------------------------------------------------------------------
 //
 // dscales[g][r] = sum_{i in g} n[r][i] dW[r][i], dW = dz^T x.  A tile is 128 outputs by
 // 256 inputs (two groups) of dW, contracted over the tokens 64 at a time; both operands come
 // straight from the row-major dz and x (contracted across their rows).  The
 // epilogue multiplies a lane's 128 sums of a group by its codes and adds them up, so dW stays in
-// tensor memory.  Two accumulators, persistent CTAs; warps 0-3 epilogue, 4 copies, 5 issues.
+// tensor memory.  The tensor core's fp32 sums are cut off, not rounded, at each of its steps of 16 tokens;
+// kSpan bounds the drift: every span of tokens has sums of its own, which the epilogue adds up.  Two accumulators, persistent CTAs; warps 0-3 epilogue, 4 copies, 5 issues.
 
 constexpr int kGradN = 256;
 constexpr int kGradB = kGradN * kChunk * 2;
 constexpr int kGradStages = 4;
+constexpr int kSpan = 16;  // stages (1,024 tokens)
 constexpr int kGradThreads = 32 * 6;
 constexpr int kGradBytes = kGradStages * (kAStage + kGradB) + 8 * (2 * kGradStages + 4) + 16 + 1024;
 
@@ -412,37 +624,47 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 
     if (warp < 4) {
         Ring<2> sums;
-        for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        bool going = true;
+        for (int64_t tile = blockIdx.x; going && tile < tiles; tile += gridDim.x) {
             const int64_t r = tile / tiles_k * kM + 32 * warp + lane, g0 = tile % tiles_k * (kGradN / kGroup);
-            if (!tc::barrier_wait_warp(sums_full(sums.slot), sums.parity, stop))
-                break;
-            tc::fence_after();
-            for (int64_t g = g0; g < g0 + kGradN / kGroup && g < w.K / kGroup; g++) {
-                const bool inside = r < w.R;
-                const int z1 = inside ? static_cast<int>((w.qzeros[(g * w.R + r) / 8] >> (4 * (r & 7))) & 15u) + 1 : 0;
-                float total = 0.0f;
-                for (int c = 0; c < kGroup; c += 32) {
-                    uint32_t v[32];
-                    __syncwarp();
-                    tc::tmem_load32(tmem + (static_cast<uint32_t>(32 * warp) << 16) + sums.slot * kGradN +
-                                        static_cast<uint32_t>(g - g0) * kGroup + c, v);
+            const bool inside = r < w.R;
+            float total[kGradN / kGroup] = {};
+            for (int64_t c0 = 0; c0 < chunks; c0 += kSpan) {
+                going = tc::barrier_wait_warp(sums_full(sums.slot), sums.parity, stop);
+                if (!going)
+                    break;
+                tc::fence_after();
 #pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        const uint32_t word = inside ? w.qweight[(g * kWordsPerGroup + c / 8 + j) * w.R + r] : 0u;
+                for (int i = 0; i < kGradN / kGroup; i++) {
+                    const int64_t g = g0 + i;
+                    if (g >= w.K / kGroup)
+                        continue;
+                    const int z1 = inside ? static_cast<int>((w.qzeros[(g * w.R + r) / 8] >> (4 * (r & 7))) & 15u) + 1 : 0;
+                    float part = 0.0f;
+                    for (int c = 0; c < kGroup; c += 32) {
+                        uint32_t word[4], v[32];
 #pragma unroll
-                        for (int i = 0; i < 8; i++)
-                            total = fmaf(__uint_as_float(v[8 * j + i]),
-                                         static_cast<float>(static_cast<int>((word >> (4 * i)) & 15u) - z1), total);
+                        for (int j = 0; j < 4; j++)
+                            word[j] = inside ? w.qweight[(g * kWordsPerGroup + c / 8 + j) * w.R + r] : 0u;
+                        __syncwarp();
+                        tc::tmem_load32(tmem + (static_cast<uint32_t>(32 * warp) << 16) + sums.slot * kGradN + i * kGroup + c, v);
+#pragma unroll
+                        for (int j = 0; j < 32; j++)
+                            part = fmaf(__uint_as_float(v[j]),
+                                        static_cast<float>(static_cast<int>((word[j / 8] >> (4 * (j % 8))) & 15u) - z1), part);
                     }
+                    total[i] += part;
                 }
-                if (inside)
-                    dscales[g * w.R + r] = total;
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    tc::barrier_arrive(sums_empty(sums.slot));
+                sums.next();
             }
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0)
-                tc::barrier_arrive(sums_empty(sums.slot));
-            sums.next();
+#pragma unroll
+            for (int i = 0; i < kGradN / kGroup; i++)
+                if (going && inside && g0 + i < w.K / kGroup)
+                    dscales[(g0 + i) * w.R + r] = total[i];
         }
     } else if (warp == 4) {
         if (lane == 0) {
@@ -472,12 +694,11 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         Ring<2> sums;
         bool going = true;
         for (int64_t tile = blockIdx.x; going && tile < tiles; tile += gridDim.x) {
-            going = tc::barrier_wait(sums_empty(sums.slot), sums.parity ^ 1, stop);
-            if (!going)
-                break;
-            tc::fence_after();
-            for (int64_t c = 0; c < chunks; c++) {
-                going = tc::barrier_wait(full(op.slot), op.parity, stop);
+            for (int64_t c = 0; going && c < chunks; c++) {
+                const bool first = c % kSpan == 0, last = c + 1 == chunks || (c + 1) % kSpan == 0;
+                if (first)
+                    going = tc::barrier_wait(sums_empty(sums.slot), sums.parity ^ 1, stop);
+                going = going && tc::barrier_wait(full(op.slot), op.parity, stop);
                 if (!going)
                     break;
                 tc::fence_after();
@@ -485,14 +706,14 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 #pragma unroll
                 for (int k = 0; k < kChunk / 16; k++)
                     tc::mma(tmem + sums.slot * kGradN, tc::descriptor(a + k * 2048, 8192, 1024),
-                            tc::descriptor(b + k * 2048, 8192, 1024), kInstr, c > 0 || k > 0);
+                            tc::descriptor(b + k * 2048, 8192, 1024), kInstr, !first || k > 0);
                 tc::commit(empty(op.slot));
                 op.next();
+                if (last) {
+                    tc::commit(sums_full(sums.slot));
+                    sums.next();
+                }
             }
-            if (!going)
-                break;
-            tc::commit(sums_full(sums.slot));
-            sums.next();
         }
     }
     __syncthreads();
@@ -635,6 +856,37 @@ cq_status product(const uint16_t *act, int64_t ld, int64_t T, const Layer &w, co
                          : run_product<D, 32, kGradient>(act, ld, T, w, ep, stream);
 }
 
+// CTAs per cluster: enough warps to keep the memory busy, at least one group for each.
+template <class D, int NT>
+cq_status few_rows(const uint16_t *x, int64_t ldx, int64_t T, const Layer &w, const Epilogue &ep, cudaStream_t stream)
+{
+    const int64_t tiles = (w.R + kFewRows - 1) / kFewRows, groups = w.K / kGroup, sms = sm_count();
+    int ranks = 1;
+    while (ranks < 8 && tiles * ranks * 2 <= 4 * sms && ranks * 2 * kFewWarps <= groups)
+        ranks *= 2;
+    cudaLaunchConfig_t config = {};
+    config.gridDim = dim3(static_cast<unsigned>(tiles * ranks));
+    config.blockDim = dim3(32 * kFewWarps);
+    config.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(ranks);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    config.attrs = attr;
+    config.numAttrs = 1;
+    return cudaLaunchKernelEx(&config, few_rows_kernel<D, NT>, x, ldx, static_cast<int>(T), w, ep) == cudaSuccess ? CQ_OK : CQ_ERR_CUDA;
+}
+
+template <class D>
+cq_status layer(const uint16_t *x, int64_t ldx, int64_t T, const Layer &w, const Epilogue &ep, cudaStream_t stream)
+{
+    if (T <= 8)
+        return few_rows<D, 1>(x, ldx, T, w, ep, stream);
+    if (T <= CQ_W4_EXACT_ROWS)
+        return few_rows<D, 2>(x, ldx, T, w, ep, stream);
+    return product<D, false>(x, ldx, T, w, ep, stream);
+}
+
 template <class D>
 cq_status scale_gradient(const uint16_t *dz, int64_t lddz, const uint16_t *x, int64_t ldx, int64_t T, const Layer &w,
                          float *dscales, cudaStream_t stream)
@@ -679,7 +931,7 @@ cq_status cq_w4_linear(const void *x, int64_t ldx, int dtype, int64_t T, const i
     const uint16_t *in = static_cast<const uint16_t *>(x);
     const Epilogue ep = {static_cast<const uint16_t *>(bias), static_cast<const uint16_t *>(residual),
                          static_cast<uint16_t *>(y), static_cast<uint16_t *>(pre), ldres, ldy, ldpre, activation};
-    return dtype == CQ_DTYPE_BF16 ? product<BF16, false>(in, ldx, T, w, ep, s) : product<FP16, false>(in, ldx, T, w, ep, s);
+    return dtype == CQ_DTYPE_BF16 ? layer<BF16>(in, ldx, T, w, ep, s) : layer<FP16>(in, ldx, T, w, ep, s);
 }
 
 cq_status cq_w4_linear_backward(const void *dz, int64_t lddz, const void *x, int64_t ldx, int dtype, int64_t T,

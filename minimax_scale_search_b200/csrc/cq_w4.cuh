@@ -64,20 +64,27 @@ __device__ __forceinline__ float half_bits(uint16_t b)
     return __half2float(__ushort_as_half(b));
 }
 
-__device__ __forceinline__ float activate(float z, int act)
+// act(z) for a result that is rounded to 16 bits: exp and the quotient to a few units of
+// 2^-22, far inside that rounding.  The quotients' limits hold: exp(-z) = inf gives 0.
+template <int n>
+__device__ __forceinline__ void activate(float (&z)[n], int act)
 {
-    constexpr float kC = 0.7978845608028654f;  // sqrt(2 / pi)
-    switch (act) {
-    case CQ_ACT_RELU:
-        return z < 0.0f ? 0.0f : z;
-    case CQ_ACT_GELU:  // erfc keeps the small values of large negative z
-        return 0.5f * z * erfcf(z * -0.7071067811865476f);
-    case CQ_ACT_GELU_TANH:
-        return 0.5f * z * (1.0f + tanhf(kC * (z + 0.044715f * z * z * z)));
-    case CQ_ACT_SILU:
-        return z / (1.0f + expf(-z));
-    default:
-        return z;
+    if (act == CQ_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < n; i++)
+            z[i] = z[i] < 0.0f ? 0.0f : z[i];
+    } else if (act == CQ_ACT_GELU) {  // erfc keeps the small values of large negative z
+#pragma unroll
+        for (int i = 0; i < n; i++)
+            z[i] = 0.5f * z[i] * erfcf(z[i] * -0.7071067811865476f);
+    } else if (act == CQ_ACT_GELU_TANH) {  // z/2 (1 + tanh u) = z / (1 + exp(-2u))
+#pragma unroll
+        for (int i = 0; i < n; i++)
+            z[i] = __fdividef(z[i], 1.0f + __expf(-1.5957691216057308f * (z[i] + 0.044715f * z[i] * z[i] * z[i])));
+    } else if (act == CQ_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < n; i++)
+            z[i] = __fdividef(z[i], 1.0f + __expf(-z[i]));
     }
 }
 
