@@ -29,8 +29,8 @@ struct Layer {
 // chunks swizzled by r mod 8.  The layer contracts along such rows, the input gradient
 // across them, so both take the same image and differ in the operand descriptor alone.
 //
-// Warps: 0-3 epilogue, 4-11 unpack, 12 copies activations (tensor map), 13 issues the
-// matrix instructions, 14 copies weights.  CTAs are persistent; two accumulators in tensor memory let
+// Warps: 0-3 epilogue, 4-19 unpack, then one that copies activations (tensor map), one that
+// issues the matrix instructions, one that copies weights.  CTAs are persistent; two accumulators in tensor memory let
 // a tile's epilogue run under the next tile's products.
 
 constexpr int kM = 128;
@@ -38,21 +38,27 @@ constexpr int kChunk = 64;                     // contraction per stage
 constexpr int kAStage = kM * kChunk * 2;
 constexpr int kRawWords = 8192;                // 16 word rows x 128 outputs
 constexpr int kRawStage = kRawWords + 512;     // and 128 scales (256 B), 16 zero words (64 B)
-constexpr int kUnpackWarps = 8;
-constexpr int kTensorThreads = 32 * 15;
+constexpr int kUnpackSets = 4, kSetWarps = 4;   // a set fills a stage
+constexpr int kUnpackWarps = kSetWarps * kUnpackSets;
+constexpr int kSetWords = kM * kChunk / 8 / (32 * kSetWarps);  // words of a stage per thread
+constexpr int kCopyWarp = 4 + kUnpackWarps, kIssueWarp = kCopyWarp + 1;
+constexpr int kTensorThreads = 32 * (kIssueWarp + 2);
 
 // Stages of (A, B) and of raw weights, by what 227 KB of shared memory hold.
 template <int N>
 struct Stages {
     static constexpr int kB = N * kChunk * 2;
-    static constexpr int kOperands = N >= 256 ? 4 : 5;
-    static constexpr int kRaw = N >= 256 ? 2 : N >= 128 ? 5 : 10;
+    static constexpr int kOperands = N >= 128 ? 4 : 5;
+    static constexpr int kRaw = N >= 256 ? 3 : N >= 128 ? 9 : 10;
     static constexpr int kBarriers = 2 * kOperands + 2 * kRaw + 4;
     static constexpr int kControl = 8 * kBarriers + 16;      // barriers, the stop flag, tensor memory's address
     static constexpr int kTurn = 4 * 16 * 33 * 4;            // the epilogue's turn from lanes to rows
     static constexpr int kBytes = kOperands * (kAStage + kB) + kRaw * kRawStage + kControl + kTurn + 1024;
     static constexpr int kColumns = 2 * N < 32 ? 32 : 2 * N;
     static_assert(kBytes <= 232448, "shared memory");
+    // A set that has filled stage c goes on to c + kUnpackSets.  It knows that c - kOperands has been read, and the
+    // parity of its next wait needs c + kUnpackSets - 2 kOperands to have been.
+    static_assert(kUnpackSets % 2 == 0 && kUnpackSets <= kOperands, "phases");
 };
 
 __device__ int g_gave_up;  // set when a wait in a kernel ran out; read by cq_w4_status
@@ -157,6 +163,11 @@ struct Ring {
             parity ^= 1;
         }
     }
+    __device__ __forceinline__ void skip(int n)
+    {
+        for (int i = 0; i < n; i++)
+            next();
+    }
 };
 
 template <class D, int N, bool kGradient>
@@ -179,20 +190,20 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
     volatile int *stop = reinterpret_cast<volatile int *>(shared + (bars - base) + 8 * S::kBarriers);
     uint32_t *tmem_at = const_cast<uint32_t *>(reinterpret_cast<volatile uint32_t *>(stop + 1));
 
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = tc::uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
     const int64_t rows = kGradient ? w.K : w.R, depth = kGradient ? (w.R + kM - 1) / kM : w.K / kM;  // in steps of 128
     const int64_t tiles_n = (T + N - 1) / N, tiles = (rows + kM - 1) / kM * tiles_n;
 
-    if (warp == 13)
+    if (warp == kIssueWarp)
         tc::tmem_alloc(tc::smem_address(tmem_at), S::kColumns);
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kOperands; i++) {
-            tc::barrier_init(full(i), kUnpackWarps + 1);
+            tc::barrier_init(full(i), kSetWarps + 1);
             tc::barrier_init(empty(i), 1);
         }
         for (int i = 0; i < S::kRaw; i++) {
             tc::barrier_init(raw_full(i), 32 + 1);
-            tc::barrier_init(raw_empty(i), kUnpackWarps);
+            tc::barrier_init(raw_empty(i), 2 * kSetWarps);
         }
         for (int i = 0; i < 2; i++) {
             tc::barrier_init(sums_full(i), 1);
@@ -208,7 +219,7 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    const uint32_t tmem = *tmem_at;
+    const uint32_t tmem = tc::uniform(*tmem_at);
 
     if (warp < 4) {
         // Epilogue, a warp's 32 m by 16 tokens at a time: a thread has one m in tensor memory;
@@ -268,48 +279,48 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
             sums.next();
         }
     } else if (warp < 4 + kUnpackWarps) {  // unpack
-        const int i = threadIdx.x - 128;
+        // Sets of warps take the stages in turn: half a group each (h).
+        const int i = threadIdx.x % (32 * kSetWarps), set = (warp - 4) / kSetWarps, h = set & 1;
+        const int r = kGradient ? h * 64 + (i & 63) : i & 127;                                 // output within the 128
+        const int k8 = kGradient ? (i >> 6) * kSetWords : h * 8 + (i >> 7) * kSetWords;        // word row within the 16
+        const uint32_t a = kGradient ? (k8 >> 3) * (kAStage / 2) + (r & 63) * 128 : r * 128;
+        const int64_t mine = static_cast<int64_t>(blockIdx.x) < tiles ? (tiles - 1 - blockIdx.x) / gridDim.x + 1 : 0;
         Ring<S::kRaw> raw;
         Ring<S::kOperands> op;
-        bool going = true;
-        for (int64_t tile = blockIdx.x; going && tile < tiles; tile += gridDim.x) {
-            for (int64_t g = 0; going && g < depth; g++) {
-                going = tc::barrier_wait_warp(raw_full(raw.slot), raw.parity, stop);
-                const char *slot = shared + (raw0 - base) + raw.slot * kRawStage;
-                const uint32_t *words = reinterpret_cast<const uint32_t *>(slot);
-                const uint16_t *scales = reinterpret_cast<const uint16_t *>(slot + kRawWords);
-                const uint32_t *zeros = reinterpret_cast<const uint32_t *>(slot + kRawWords + 256);
+        raw.skip(set / 2);
+        op.skip(set);
+        for (int64_t g = set / 2; g < mine * depth; g += kUnpackSets / 2) {
+            if (!tc::barrier_wait_warp(raw_full(raw.slot), raw.parity, stop))
+                break;
+            const char *slot = shared + (raw0 - base) + raw.slot * kRawStage;
+            const uint32_t *words = reinterpret_cast<const uint32_t *>(slot) + k8 * kM + r;
+            const Unpack<D> unpack(reinterpret_cast<const uint16_t *>(slot + kRawWords)[r],
+                                   (reinterpret_cast<const uint32_t *>(slot + kRawWords + 256)[r >> 3] >> (4 * (r & 7))) & 15u);
+            uint32_t word[kSetWords];
 #pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    if (!going)
-                        break;
-                    // layer: 128 outputs x 8 word rows; gradient: 64 outputs x 16 word rows
-                    const int r = kGradient ? h * 64 + (i & 63) : i & 127;
-                    const int k8 = kGradient ? (i >> 6) * 4 : h * 8 + (i >> 7) * 4;
-                    const Unpack<D> unpack(scales[r], (zeros[r >> 3] >> (4 * (r & 7))) & 15u);
-                    uint32_t word[4];
+            for (int j = 0; j < kSetWords; j++)
+                word[j] = words[j * kM];
+            __syncwarp();
+            if (lane == 0)
+                tc::barrier_arrive(raw_empty(raw.slot));
+            raw.skip(kUnpackSets / 2);
+            uint4 values[kSetWords];
 #pragma unroll
-                    for (int j = 0; j < 4; j++)
-                        word[j] = words[(k8 + j) * kM + r];
-                    going = tc::barrier_wait_warp(empty(op.slot), op.parity ^ 1, stop);
-                    if (!going)
-                        break;
-                    char *a = shared + (a_at(op.slot) - base) + (kGradient ? (k8 >> 3) * (kAStage / 2) + (i & 63) * 128 : r * 128);
+            for (int j = 0; j < kSetWords; j++)
+                values[j] = unpack(word[j]);
+            if (!tc::barrier_wait_warp(empty(op.slot), op.parity ^ 1, stop))
+                break;
+            char *to = shared + (a_at(op.slot) - base) + a;
 #pragma unroll
-                    for (int j = 0; j < 4; j++)
-                        *reinterpret_cast<uint4 *>(a + (((k8 + j) & 7) ^ (r & 7)) * 16) = unpack(word[j]);
-                    tc::fence_shared_writes();
-                    __syncwarp();
-                    if (lane == 0)
-                        tc::barrier_arrive(full(op.slot));
-                    op.next();
-                }
-                if (going && lane == 0)
-                    tc::barrier_arrive(raw_empty(raw.slot));
-                raw.next();
-            }
+            for (int j = 0; j < kSetWords; j++)
+                *reinterpret_cast<uint4 *>(to + (((k8 + j) & 7) ^ (r & 7)) * 16) = values[j];
+            tc::fence_shared_writes();
+            __syncwarp();
+            if (lane == 0)
+                tc::barrier_arrive(full(op.slot));
+            op.skip(kUnpackSets);
         }
-    } else if (warp == 12) {  // activations
+    } else if (warp == kCopyWarp) {  // activations
         if (lane == 0) {
             Ring<S::kOperands> op;
             bool going = true;
@@ -325,37 +336,52 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
                 }
             }
         }
-    } else if (warp == 13) {  // matrix instructions
-        if (lane == 0) {
-            constexpr uint32_t kInstr = tc::instruction(D::kMagic == BF16::kMagic, kGradient, false, N);
-            Ring<S::kOperands> op;
-            Ring<2> sums;
-            bool going = true;
-            for (int64_t tile = blockIdx.x; going && tile < tiles; tile += gridDim.x) {
-                going = tc::barrier_wait(sums_empty(sums.slot), sums.parity ^ 1, stop);
+    } else if (warp == kIssueWarp) {  // matrix instructions: the loop is the whole warp's, so that what it computes stays uniform
+        constexpr uint32_t kInstr = tc::instruction(D::kMagic == BF16::kMagic, kGradient, false, N);
+        constexpr uint32_t kStep = kGradient ? 2048 : 32;  // 16 of the contraction in A: 16 rows, or 32 bytes of a row
+        const uint64_t a_first = tc::descriptor(base, kGradient ? kAStage / 2 : 16, 1024);
+        const uint64_t b_first = tc::descriptor(base + kAStage, 16, 1024);
+        const int64_t mine = static_cast<int64_t>(blockIdx.x) < tiles ? (tiles - 1 - blockIdx.x) / gridDim.x + 1 : 0;
+        const uint32_t stages = static_cast<uint32_t>(2 * depth);
+        Ring<2> sums;
+        uint32_t parity = 0, c = 0;
+        int64_t left = mine;
+        bool going = left > 0;
+        while (going) {
+#pragma unroll
+            for (int slot = 0; slot < S::kOperands; slot++) {  // unrolled: addresses and descriptors stay fixed
+                if (c == 0) {
+                    going = going && tc::barrier_wait_warp(sums_empty(sums.slot), sums.parity ^ 1, stop);
+                    tc::fence_after();
+                }
+                going = going && tc::barrier_wait_warp(full(slot), parity, stop);
                 if (!going)
                     break;
                 tc::fence_after();
-                for (int64_t c = 0; c < 2 * depth; c++) {
-                    going = tc::barrier_wait(full(op.slot), op.parity, stop);
-                    if (!going)
-                        break;
-                    tc::fence_after();
-                    const uint32_t a = a_at(op.slot), b = a + kAStage;
+                const uint64_t a = a_first + static_cast<uint32_t>(slot * (kAStage + S::kB) / 16);
+                const uint64_t b = b_first + static_cast<uint32_t>(slot * (kAStage + S::kB) / 16);
+                const uint32_t d = tmem + sums.slot * N;
+                const bool last = ++c == stages;
+                if (tc::elected()) {
+                    tc::mma(d, a, b, kInstr, c > 1);
 #pragma unroll
-                    for (int k = 0; k < kChunk / 16; k++) {
-                        const uint64_t da = kGradient ? tc::descriptor(a + k * 2048, kAStage / 2, 1024)
-                                                      : tc::descriptor(a + k * 32, 16, 1024);
-                        tc::mma(tmem + sums.slot * N, da, tc::descriptor(b + k * 32, 16, 1024), kInstr, c > 0 || k > 0);
-                    }
-                    tc::commit(empty(op.slot));
-                    op.next();
+                    for (int k = 1; k < kChunk / 16; k++)
+                        tc::mma_add(d, a + k * (kStep / 16), b + k * (32 / 16), kInstr);
+                    tc::commit(empty(slot));
+                    if (last)
+                        tc::commit(sums_full(sums.slot));
                 }
-                if (!going)
-                    break;
-                tc::commit(sums_full(sums.slot));
-                sums.next();
+                __syncwarp();
+                if (last) {
+                    c = 0;
+                    sums.next();
+                    if (--left == 0) {
+                        going = false;
+                        break;
+                    }
+                }
             }
+            parity ^= 1;
         }
     } else {  // weights
         Ring<S::kRaw> raw;
@@ -389,7 +415,7 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
         tc::let_copies_land();
         g_gave_up = 1;
     }
-    if (warp == 13)
+    if (warp == kIssueWarp)
         tc::tmem_free(tmem, S::kColumns);
 }
 
@@ -599,7 +625,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     volatile int *stop = reinterpret_cast<volatile int *>(shared + (bars - base) + 8 * (2 * kGradStages + 4));
     uint32_t *tmem_at = const_cast<uint32_t *>(reinterpret_cast<volatile uint32_t *>(stop + 1));
 
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = tc::uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
     const int64_t tiles_k = (w.K + kGradN - 1) / kGradN, tiles = (w.R + kM - 1) / kM * tiles_k;
     const int64_t chunks = (T + kChunk - 1) / kChunk;
 
@@ -620,7 +646,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    const uint32_t tmem = *tmem_at;
+    const uint32_t tmem = tc::uniform(*tmem_at);
 
     if (warp < 4) {
         Ring<2> sums;
@@ -688,8 +714,9 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                 }
             }
         }
-    } else if (lane == 0) {
+    } else {
         constexpr uint32_t kInstr = tc::instruction(D::kMagic == BF16::kMagic, true, true, kGradN);
+        const uint64_t a_first = tc::descriptor(base, 8192, 1024), b_first = tc::descriptor(base + kAStage, 8192, 1024);
         Ring<kGradStages> op;
         Ring<2> sums;
         bool going = true;
@@ -697,22 +724,27 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             for (int64_t c = 0; going && c < chunks; c++) {
                 const bool first = c % kSpan == 0, last = c + 1 == chunks || (c + 1) % kSpan == 0;
                 if (first)
-                    going = tc::barrier_wait(sums_empty(sums.slot), sums.parity ^ 1, stop);
-                going = going && tc::barrier_wait(full(op.slot), op.parity, stop);
+                    going = tc::barrier_wait_warp(sums_empty(sums.slot), sums.parity ^ 1, stop);
+                going = going && tc::barrier_wait_warp(full(op.slot), op.parity, stop);
                 if (!going)
                     break;
                 tc::fence_after();
-                const uint32_t a = a_at(op.slot), b = a + kAStage;
+                const uint32_t d = tmem + sums.slot * kGradN;
+                const uint64_t a = a_first + static_cast<uint32_t>(op.slot * (kAStage + kGradB) / 16);
+                const uint64_t b = b_first + static_cast<uint32_t>(op.slot * (kAStage + kGradB) / 16);
+                if (tc::elected()) {
+                    tc::mma(d, a, b, kInstr, !first);
 #pragma unroll
-                for (int k = 0; k < kChunk / 16; k++)
-                    tc::mma(tmem + sums.slot * kGradN, tc::descriptor(a + k * 2048, 8192, 1024),
-                            tc::descriptor(b + k * 2048, 8192, 1024), kInstr, !first || k > 0);
-                tc::commit(empty(op.slot));
-                op.next();
-                if (last) {
-                    tc::commit(sums_full(sums.slot));
-                    sums.next();
+                    for (int k = 1; k < kChunk / 16; k++)
+                        tc::mma_add(d, a + k * 128, b + k * 128, kInstr);
+                    tc::commit(empty(op.slot));
+                    if (last)
+                        tc::commit(sums_full(sums.slot));
                 }
+                __syncwarp();
+                op.next();
+                if (last)
+                    sums.next();
             }
         }
     }
@@ -835,8 +867,8 @@ cq_status run_product(const uint16_t *act, int64_t ld, int64_t T, const Layer &w
     return launched();
 }
 
-// Tokens per tile: the least time by a count of waves, where a stage of N tokens takes the tensor
-// core 2 N cycles and the unpacking warps about 200.
+// Tokens per tile: the least time by a count of waves, a stage of N tokens costing 2 N cycles on the tensor
+// core but never less than about 450, what the chain of waits between the warps takes.
 template <class D, bool kGradient>
 cq_status product(const uint16_t *act, int64_t ld, int64_t T, const Layer &w, const Epilogue &ep, cudaStream_t stream)
 {
@@ -844,7 +876,7 @@ cq_status product(const uint16_t *act, int64_t ld, int64_t T, const Layer &w, co
     int64_t least = INT64_MAX;
     int best = 256;
     for (int n = 256; n >= 32; n /= 2) {
-        const int64_t waves = (m * ((T + n - 1) / n) + sms - 1) / sms, cost = waves * (2 * n > 200 ? 2 * n : 200);
+        const int64_t waves = (m * ((T + n - 1) / n) + sms - 1) / sms, cost = waves * (2 * n > 450 ? 2 * n : 450);
         if (cost < least) {
             least = cost;
             best = n;

@@ -15,6 +15,21 @@ __device__ __forceinline__ uint32_t smem_address(const void *p)
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// A value that is the same in all lanes, in a form that the compiler knows to be: branches on it are
+// uniform, and addresses and descriptors made of it stay in uniform registers.
+__device__ __forceinline__ uint32_t uniform(uint32_t v)
+{
+    return __shfl_sync(0xFFFFFFFFu, v, 0);
+}
+
+// One lane of the warp: the one that issues for all.
+__device__ __forceinline__ bool elected()
+{
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.b32 %0, 1, 0, p;\n}" : "=r"(p));
+    return p != 0;
+}
+
 // ---- mbarriers ---------------------------------------------------------------------------------
 
 __device__ __forceinline__ void barrier_init(uint32_t bar, uint32_t count)
@@ -158,6 +173,15 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
         "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
         " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_add(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc)
+{
+    asm volatile(
+        "{\n .reg .pred p;\n setp.eq.u32 p, 0, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc)
         : "memory");
 }
 
