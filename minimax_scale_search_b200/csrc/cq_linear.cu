@@ -29,19 +29,19 @@ struct Layer {
 // chunks swizzled by r mod 8.  The layer contracts along such rows, the input gradient
 // across them, so both take the same image and differ in the operand descriptor alone.
 //
-// Warps: 0-3 epilogue, 4-19 unpack, then one that copies activations (tensor map), one that
-// issues the matrix instructions, one that copies weights.  CTAs are persistent; two accumulators in tensor memory let
+// Warps: 0-3 epilogue, 4-19 unpack, then one each that copies activations, copies words, issues the matrix
+// instructions, copies scales and zero points.  CTAs are persistent; two accumulators in tensor memory let
 // a tile's epilogue run under the next tile's products.
 
 constexpr int kM = 128;
 constexpr int kChunk = 64;                     // contraction per stage
 constexpr int kAStage = kM * kChunk * 2;
-constexpr int kRawWords = 8192;                // 16 word rows x 128 outputs
-constexpr int kRawStage = kRawWords + 512;     // and 128 scales (256 B), 16 zero words (64 B)
+constexpr int kRawWords = 4096;                // a stage's words: 8 word rows x 128 outputs, or 16 x 64
+constexpr int kRawStage = kRawWords + 512;     // and up to 128 scales (256 B) and 16 zero words (64 B)
 constexpr int kUnpackSets = 4, kSetWarps = 4;   // a set fills a stage
 constexpr int kUnpackWarps = kSetWarps * kUnpackSets;
 constexpr int kSetWords = kM * kChunk / 8 / (32 * kSetWarps);  // words of a stage per thread
-constexpr int kCopyWarp = 4 + kUnpackWarps, kIssueWarp = kCopyWarp + 1;
+constexpr int kCopyWarp = 4 + kUnpackWarps, kWordWarp = kCopyWarp + 1, kIssueWarp = kWordWarp + 1;
 constexpr int kTensorThreads = 32 * (kIssueWarp + 2);
 
 // Stages of (A, B) and of raw weights, by what 227 KB of shared memory hold.
@@ -49,7 +49,7 @@ template <int N>
 struct Stages {
     static constexpr int kB = N * kChunk * 2;
     static constexpr int kOperands = N >= 128 ? 4 : 5;
-    static constexpr int kRaw = N >= 256 ? 3 : N >= 128 ? 9 : 10;
+    static constexpr int kRaw = N >= 256 ? 4 : 16;
     static constexpr int kBarriers = 2 * kOperands + 2 * kRaw + 4;
     static constexpr int kControl = 8 * kBarriers + 16;      // barriers, the stop flag, tensor memory's address
     static constexpr int kTurn = 4 * 16 * 33 * 4;            // the epilogue's turn from lanes to rows
@@ -59,6 +59,9 @@ struct Stages {
     // A set that has filled stage c goes on to c + kUnpackSets.  It knows that c - kOperands has been read, and the
     // parity of its next wait needs c + kUnpackSets - 2 kOperands to have been.
     static_assert(kUnpackSets % 2 == 0 && kUnpackSets <= kOperands, "phases");
+    // A slot of raw weights belongs to one set: loads complete in any order, so only the set that has read a slot
+    // before knows which of its phases the next wait is for.
+    static_assert(kRaw % kUnpackSets == 0, "phases");
 };
 
 __device__ int g_gave_up;  // set when a wait in a kernel ran out; read by cq_w4_status
@@ -203,7 +206,7 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
         }
         for (int i = 0; i < S::kRaw; i++) {
             tc::barrier_init(raw_full(i), 32 + 1);
-            tc::barrier_init(raw_empty(i), 2 * kSetWarps);
+            tc::barrier_init(raw_empty(i), kSetWarps);
         }
         for (int i = 0; i < 2; i++) {
             tc::barrier_init(sums_full(i), 1);
@@ -279,31 +282,35 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
             sums.next();
         }
     } else if (warp < 4 + kUnpackWarps) {  // unpack
-        // Sets of warps take the stages in turn: half a group each (h).
-        const int i = threadIdx.x % (32 * kSetWarps), set = (warp - 4) / kSetWarps, h = set & 1;
-        const int r = kGradient ? h * 64 + (i & 63) : i & 127;                                 // output within the 128
-        const int k8 = kGradient ? (i >> 6) * kSetWords : h * 8 + (i >> 7) * kSetWords;        // word row within the 16
-        const uint32_t a = kGradient ? (k8 >> 3) * (kAStage / 2) + (r & 63) * 128 : r * 128;
-        const int64_t mine = static_cast<int64_t>(blockIdx.x) < tiles ? (tiles - 1 - blockIdx.x) / gridDim.x + 1 : 0;
-        Ring<S::kRaw> raw;
+        // Sets of warps take the stages in turn.
+        const int i = threadIdx.x % (32 * kSetWarps), set = (warp - 4) / kSetWarps;
+        constexpr int kOutputs = kGradient ? 64 : kM;       // outputs of a stage
+        const int r = i % kOutputs, k8 = i / kOutputs * kSetWords;  // output and first word row within it
+        const uint32_t a = kGradient ? (k8 >> 3) * (kAStage / 2) + r * 128 : r * 128;
+        const int64_t stages = (static_cast<int64_t>(blockIdx.x) < tiles ? (tiles - 1 - blockIdx.x) / gridDim.x + 1 : 0) * 2 * depth;
+        int raw = set;
+        uint32_t raw_parity = 0;
         Ring<S::kOperands> op;
-        raw.skip(set / 2);
         op.skip(set);
-        for (int64_t g = set / 2; g < mine * depth; g += kUnpackSets / 2) {
-            if (!tc::barrier_wait_warp(raw_full(raw.slot), raw.parity, stop))
+        for (int64_t c = set; c < stages; c += kUnpackSets) {
+            if (!tc::barrier_wait_warp(raw_full(raw), raw_parity, stop))
                 break;
-            const char *slot = shared + (raw0 - base) + raw.slot * kRawStage;
-            const uint32_t *words = reinterpret_cast<const uint32_t *>(slot) + k8 * kM + r;
+            const char *slot = shared + (raw0 - base) + raw * kRawStage;
+            const uint32_t *words = reinterpret_cast<const uint32_t *>(slot) + k8 * kOutputs + r;
             const Unpack<D> unpack(reinterpret_cast<const uint16_t *>(slot + kRawWords)[r],
                                    (reinterpret_cast<const uint32_t *>(slot + kRawWords + 256)[r >> 3] >> (4 * (r & 7))) & 15u);
             uint32_t word[kSetWords];
 #pragma unroll
             for (int j = 0; j < kSetWords; j++)
-                word[j] = words[j * kM];
+                word[j] = words[j * kOutputs];
             __syncwarp();
             if (lane == 0)
-                tc::barrier_arrive(raw_empty(raw.slot));
-            raw.skip(kUnpackSets / 2);
+                tc::barrier_arrive(raw_empty(raw));
+            raw += kUnpackSets;
+            if (raw >= S::kRaw) {
+                raw -= S::kRaw;
+                raw_parity ^= 1;
+            }
             uint4 values[kSetWords];
 #pragma unroll
             for (int j = 0; j < kSetWords; j++)
@@ -320,20 +327,41 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
                 tc::barrier_arrive(full(op.slot));
             op.skip(kUnpackSets);
         }
-    } else if (warp == kCopyWarp) {  // activations
-        if (lane == 0) {
-            Ring<S::kOperands> op;
-            bool going = true;
-            for (int64_t tile = blockIdx.x; going && tile < tiles; tile += gridDim.x) {
-                const int t0 = static_cast<int>(tile % tiles_n * N);
-                for (int64_t c = 0; c < 2 * depth; c++) {
-                    going = tc::barrier_wait(empty(op.slot), op.parity ^ 1, stop);
-                    if (!going)
-                        break;
+    } else if (warp == kCopyWarp) {  // activations, by tensor map
+        Ring<S::kOperands> op;
+        bool going = true;
+        for (int64_t tile = blockIdx.x; going && tile < tiles; tile += gridDim.x) {
+            const int t0 = static_cast<int>(tile % tiles_n * N), end = static_cast<int>(2 * depth) * kChunk;
+            for (int c = 0; c < end; c += kChunk) {
+                going = tc::barrier_wait_warp(empty(op.slot), op.parity ^ 1, stop);
+                if (!going)
+                    break;
+                if (tc::elected()) {
                     tc::barrier_expect(full(op.slot), S::kB);
-                    tc::copy_box(a_at(op.slot) + kAStage, &act_map, static_cast<int>(c * kChunk), t0, full(op.slot));
-                    op.next();
+                    tc::copy_box(a_at(op.slot) + kAStage, &act_map, c, t0, full(op.slot));
                 }
+                __syncwarp();
+                op.next();
+            }
+        }
+    } else if (warp == kWordWarp) {  // words, by tensor map
+        Ring<S::kRaw> raw;
+        bool going = true;
+        for (int64_t tile = blockIdx.x; going && tile < tiles; tile += gridDim.x) {
+            const int m0 = static_cast<int>(tile / tiles_n * kM);
+            int r = kGradient ? 0 : m0, row = kGradient ? m0 / 8 : 0;
+            for (int c = 0; c < static_cast<int>(2 * depth); c++) {
+                going = tc::barrier_wait_warp(raw_empty(raw.slot), raw.parity ^ 1, stop);
+                if (!going)
+                    break;
+                if (tc::elected()) {
+                    tc::barrier_expect(raw_full(raw.slot), kRawWords);
+                    tc::copy_box(raw0 + raw.slot * kRawStage, &word_map, r, row, raw_full(raw.slot));
+                }
+                __syncwarp();
+                r += kGradient ? kChunk : 0;
+                row += kGradient ? 0 : kChunk / 8;
+                raw.next();
             }
         }
     } else if (warp == kIssueWarp) {  // matrix instructions: the loop is the whole warp's, so that what it computes stays uniform
@@ -383,28 +411,38 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
             }
             parity ^= 1;
         }
-    } else {  // weights
+    } else {  // half the lanes 16 bytes (8 outputs) of scales, half a word of zero points
         Ring<S::kRaw> raw;
+        const int l = lane & 15;
+        const uint32_t to = raw0 + kRawWords + (lane < 16 ? 16 * l : 256 + 4 * l);
+        const bool mine = !kGradient || l < 8;
+        const int64_t group_step = lane < 16 ? 2 * w.R : w.R / 2;
         bool going = true;
         for (int64_t tile = blockIdx.x; going && tile < tiles; tile += gridDim.x) {
             const int64_t m0 = tile / tiles_n * kM;
-            for (int64_t g = 0; g < depth; g++) {
+            int64_t r = (kGradient ? 0 : m0) + 8 * l;
+            const int64_t group = kGradient ? m0 / kGroup : 0;
+            const char *from = lane < 16 ? reinterpret_cast<const char *>(w.scales + group * w.R + r)
+                                         : reinterpret_cast<const char *>(w.qzeros + (group * w.R + r) / 8);
+            for (int c = 0; c < static_cast<int>(2 * depth); c++) {
                 going = tc::barrier_wait_warp(raw_empty(raw.slot), raw.parity ^ 1, stop);
                 if (!going)
                     break;
-                const int64_t r0 = kGradient ? g * kM : m0, group = kGradient ? m0 / kGroup : g;
-                const uint32_t at = raw0 + raw.slot * kRawStage;
-                if (lane == 0) {
-                    tc::barrier_expect(raw_full(raw.slot), kRawWords);
-                    tc::copy_box(at, &word_map, static_cast<int>(r0), static_cast<int>(group * kWordsPerGroup), raw_full(raw.slot));
+                if (mine) {
+                    const bool inside = r < w.R;
+                    const char *p = inside ? from : reinterpret_cast<const char *>(w.scales);
+                    if (lane < 16)
+                        tc::copy_async<16>(to + raw.slot * kRawStage, p, inside);
+                    else
+                        tc::copy_async<4>(to + raw.slot * kRawStage, p, inside);
                 }
-                const int64_t r = r0 + 8 * (lane & 15);  // 8 outputs: a 16-byte run of scales, a word of zeros
-                const bool inside = r < w.R;
-                if (lane < 16)
-                    tc::copy_async<16>(at + kRawWords + 16 * lane, w.scales + (inside ? group * w.R + r : 0), inside);
-                else
-                    tc::copy_async<4>(at + kRawWords + 256 + 4 * (lane - 16), w.qzeros + (inside ? (group * w.R + r) / 8 : 0), inside);
                 tc::copy_async_arrive(raw_full(raw.slot));
+                if (kGradient) {
+                    r += kChunk;
+                    from += lane < 16 ? kChunk * 2 : kChunk / 2;
+                } else if (c & 1) {
+                    from += group_step;
+                }
                 raw.next();
             }
         }
@@ -421,16 +459,32 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
 
 // ---- few rows ----------------------------------------------------------------------------------
 //
-// Up to 16 rows the weights' bytes are the work: a CTA has 32 outputs, its 8 warps (of all
-// the CTAs of a cluster) take the groups in turn.  A thread loads 4 outputs' words at once (16 bytes,
-// 4 lanes of a word row make 128-byte runs over 8 lanes); a word is 8 inputs, whose pairs (q, q + 4)
-// come out of it with a shift and a mask.  That order of the inputs is as good as any for the
-// m16n8k16 product if the activations' pairs are the same.  The codes enter as integers and each
-// group's fp32 sum is scaled after, so the weights are exact.
-// The warps' and the cluster's sums meet in shared memory in a fixed order.
+// Up to 16 rows the weights' bytes are the work.  A CTA has 128 outputs and a part of the groups (a
+// cluster has them all); one warp keeps a ring of groups in flight (words by tensor map, scales, zero
+// points and the tokens' 128 inputs by asynchronous copies), eight warps in four sets take them in turn,
+// 64 outputs a warp.  A thread reads 4 adjacent outputs' words at once; a word is 8 inputs, whose pairs
+// (q, q + 4) come out of it with a shift and a mask.  That order of the inputs is as good as any for the
+// m16n8k16 product if the activations' pairs are the same.  The codes enter as integers, zero point
+// taken off, and each group's fp32 sum is scaled after, so the weights are exact.  The sets' and the
+// cluster's sums meet in shared memory in a fixed order.
 
-constexpr int kFewWarps = 8;
-constexpr int kFewRows = 32;   // outputs per CTA
+constexpr int kFewSets = 4;
+constexpr int kFewWords = 8192;                // 16 word rows x 128 outputs
+constexpr int kFewThreads = 32 * (2 * kFewSets + 2);
+constexpr int kFewX = kFewWords + 320;       // a stage: words, 256 B of scales, 64 B of zero points, inputs
+constexpr int kFewXRow = 272;                // a token's 128 inputs; 16 bytes more keep two rows' reads off each other's banks
+
+template <int NT>
+struct FewStages {
+    static constexpr int kStage = (kFewX + 8 * NT * kFewXRow + 1023) / 1024 * 1024;
+    static constexpr int kStages = 8;
+    static constexpr int kBytes = kStages * kStage + 16 * kStages + 16 + 1024;
+    static_assert(2 * (kBytes + 1024) <= 228 * 1024, "two CTAs an SM");
+    static_assert((kFewSets + 1) * 8 * NT * kM * 4 <= kStages * kStage, "sums reuse the ring");
+    // A stage belongs to one set: loads complete in any order, so only the set that has read a stage before
+    // knows which of its phases the next wait is for.
+    static_assert(kStages % kFewSets == 0, "phases");
+};
 
 template <class D>
 __device__ __forceinline__ void mma_16x8x16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
@@ -453,140 +507,214 @@ __device__ __forceinline__ void mma_16x8x16<FP16>(float (&d)[4], const uint32_t 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// What a thread needs of one group: 4 word rows of its 4 outputs, their scales and
-// zero points, and 32 inputs of one token of each tile of 8.
-template <int NT>
-struct GroupData {
-    uint4 words[4];
-    uint2 scales;
-    uint32_t zeros;
-    uint4 x[NT][4];
-};
-
 template <class D, int NT>
-__global__ void __launch_bounds__(32 * kFewWarps)
-    few_rows_kernel(const uint16_t *__restrict__ x, int64_t ldx, int T, Layer w, Epilogue ep)
+__global__ void __launch_bounds__(kFewThreads, 2)
+    few_rows_kernel(const __grid_constant__ CUtensorMap word_map, const uint16_t *__restrict__ x, int64_t ldx, int T, Layer w,
+                    Epilogue ep)
 {
-    __shared__ float sums[kFewWarps][8 * NT * kFewRows];
-    __shared__ float cta_sums[8 * NT * kFewRows];
+    using S = FewStages<NT>;
+    extern __shared__ char shared_raw[];
+    const uint32_t base = (tc::smem_address(shared_raw) + 1023) & ~1023u;
+    char *shared = shared_raw + (base - tc::smem_address(shared_raw));
+    const uint32_t bars = base + S::kStages * S::kStage;
+    auto full = [&](int i) { return bars + 8 * i; };
+    auto empty = [&](int i) { return bars + 8 * (S::kStages + i); };
+    volatile int *stop = reinterpret_cast<volatile int *>(shared + (bars - base) + 16 * S::kStages);
+
     cg::cluster_group cluster = cg::this_cluster();
     const int ranks = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int quad = lane >> 2, c = lane & 3;
-    const int64_t r0 = static_cast<int64_t>(blockIdx.x / ranks) * kFewRows, r = r0 + 4 * quad;
-    const bool inside = r < w.R;  // R % 8 == 0: four outputs in or out together
-    const int64_t groups = w.K / kGroup;
+    const int warp = tc::uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
+    const int64_t r0 = static_cast<int64_t>(blockIdx.x / ranks) * kM;
+    const int groups = static_cast<int>(w.K / kGroup);
+    const int first = static_cast<int>(static_cast<int64_t>(groups) * rank / ranks);
+    const int count = static_cast<int>(static_cast<int64_t>(groups) * (rank + 1) / ranks) - first;
 
-    auto load = [&](int64_t g, GroupData<NT> &d) {
-#pragma unroll
-        for (int j = 0; j < 4; j++)
-            d.words[j] = inside ? __ldcs(reinterpret_cast<const uint4 *>(w.qweight + (g * kWordsPerGroup + 4 * j + c) * w.R + r))
-                                : make_uint4(0, 0, 0, 0);
-        d.scales = inside ? *reinterpret_cast<const uint2 *>(w.scales + g * w.R + r) : make_uint2(0, 0);
-        d.zeros = inside ? w.qzeros[(g * w.R + r) / 8] >> (4 * (r & 7)) : 0u;
-#pragma unroll
-        for (int n = 0; n < NT; n++)
-#pragma unroll
-            for (int j = 0; j < 4; j++)
-                d.x[n][j] = 8 * n + quad < T
-                                ? *reinterpret_cast<const uint4 *>(x + (8 * n + quad) * ldx + g * kGroup + 8 * (4 * j + c))
-                                : make_uint4(0, 0, 0, 0);
-    };
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::kStages; i++) {
+            tc::barrier_init(full(i), 32 + 1);
+            tc::barrier_init(empty(i), 2);
+        }
+        *stop = 0;
+        tc::barrier_init_fence();
+    }
+    for (int i = threadIdx.x; i < S::kStages * (8 * NT - T) * 16; i += kFewThreads) {  // rows of no token: zeros, never written again
+        const int stage = i / ((8 * NT - T) * 16), row = T + i / 16 % (8 * NT - T);
+        *reinterpret_cast<uint4 *>(shared + stage * S::kStage + kFewX + row * kFewXRow + i % 16 * 16) = make_uint4(0, 0, 0, 0);
+    }
+    __syncthreads();
 
-    float total[2][NT][4] = {};
-    auto multiply = [&](const GroupData<NT> &d) {
-        float acc[2][NT][4] = {};
-        uint32_t zero[4];
+    float total[4][NT][4] = {};
+    const int half = warp & 1, quad = lane >> 2, c = lane & 3;
+    if (warp == 2 * kFewSets) {  // words
+        Ring<S::kStages> ring;
+        int row = first * kWordsPerGroup;
+        for (int i = 0; i < count; i++) {
+            if (!tc::barrier_wait_warp(empty(ring.slot), ring.parity ^ 1, stop))
+                break;
+            if (tc::elected()) {
+                tc::barrier_expect(full(ring.slot), kFewWords);
 #pragma unroll
-        for (int i = 0; i < 4; i++)
-            zero[i] = zero_pair<D>((d.zeros >> (4 * i)) & 15u);
+                for (int b = 0; b < 4; b++)  // 32 outputs x 16 word rows, swizzled
+                    tc::copy_box(base + ring.slot * S::kStage + 2048 * b, &word_map, static_cast<int>(r0) + 32 * b, row, full(ring.slot));
+            }
+            __syncwarp();
+            row += kWordsPerGroup;
+            ring.next();
+        }
+    } else if (warp == 2 * kFewSets + 1) {  // the rest: half the lanes 16 bytes of scales, half a word of zero points; inputs by all
+        Ring<S::kStages> ring;
+        const int l = lane & 15;
+        const bool inside = r0 + 8 * l < w.R;
+        const int64_t at = static_cast<int64_t>(first) * w.R + (inside ? r0 + 8 * l : 0);
+        const char *from = lane < 16 ? reinterpret_cast<const char *>(w.scales + at) : reinterpret_cast<const char *>(w.qzeros + at / 8);
+        const int64_t step = lane < 16 ? 2 * w.R : w.R / 2;
+        const uint32_t to = kFewWords + (lane < 16 ? 16 * l : 256 + 4 * l);
+        const char *in = reinterpret_cast<const char *>(x + (lane >> 4) * ldx + static_cast<int64_t>(first) * kGroup + 8 * l);
+        const int64_t rows = 4 * ldx;
+        for (int i = 0; i < count; i++) {
+            if (!tc::barrier_wait_warp(empty(ring.slot), ring.parity ^ 1, stop))
+                break;
+            const uint32_t stage = base + ring.slot * S::kStage;
+            if (lane < 16)
+                tc::copy_async<16>(stage + to, from, inside);
+            else
+                tc::copy_async<4>(stage + to, from, inside);
+            const char *p = in;
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const uint32_t word[4] = {d.words[j].x, d.words[j].y, d.words[j].z, d.words[j].w};
-            uint32_t pair[4][4];  // [output][q]: inputs q and q + 4
+            for (int n = 0; n < 4 * NT; n++) {
+                if (2 * n + (lane >> 4) < T)
+                    tc::copy_async<16>(stage + kFewX + (2 * n + (lane >> 4)) * kFewXRow + 16 * l, p, true);
+                p += rows;
+            }
+            tc::copy_async_arrive(full(ring.slot));
+            if (inside)
+                from += step;
+            in += 2 * kGroup;
+            ring.next();
+        }
+        tc::copy_async_wait();
+    } else {
+        int slot = warp / 2;
+        uint32_t parity = 0;
+        for (int i = warp / 2; i < count; i += kFewSets) {
+            if (!tc::barrier_wait_warp(full(slot), parity, stop))
+                break;
+            const char *at = shared + slot * S::kStage;
+            float acc[4][NT][4] = {};
+            uint32_t zero[2][4];
 #pragma unroll
-            for (int i = 0; i < 4; i++)
+            for (int m = 0; m < 2; m++) {
+                const uint32_t z = reinterpret_cast<const uint32_t *>(at + kFewWords + 256)[8 * half + 4 * m + quad / 2] >> (16 * (quad & 1));
 #pragma unroll
-                for (int q = 0; q < 4; q++)
-                    pair[i][q] = D::sub(((word[i] >> (4 * q)) & 0x000F000Fu) | D::kMagic, zero[i]);
+                for (int k = 0; k < 4; k++)
+                    zero[m][k] = zero_pair<D>((z >> (4 * k)) & 15u);
+            }
 #pragma unroll
-            for (int n = 0; n < NT; n++) {
-                const uint4 v = d.x[n][j];
-                const uint32_t b[4] = {__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
-                                       __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632)};
+            for (int j = 0; j < 4; j++) {
+                const int k8 = 8 * (j >> 1) + 2 * c + (j & 1);  // this order of word rows keeps a warp's reads on all banks
+                uint32_t b[NT][4];
 #pragma unroll
-                for (int p = 0; p < 2; p++) {
+                for (int n = 0; n < NT; n++) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(at + kFewX + (8 * n + quad) * kFewXRow + 16 * k8);
+                    b[n][0] = __byte_perm(v.x, v.z, 0x5410);
+                    b[n][1] = __byte_perm(v.x, v.z, 0x7632);
+                    b[n][2] = __byte_perm(v.y, v.w, 0x5410);
+                    b[n][3] = __byte_perm(v.y, v.w, 0x7632);
+                }
 #pragma unroll
-                    for (int s = 0; s < 2; s++) {
-                        const uint32_t a[4] = {pair[2 * p][2 * s], pair[2 * p + 1][2 * s], pair[2 * p][2 * s + 1],
-                                               pair[2 * p + 1][2 * s + 1]};
-                        mma_16x8x16<D>(acc[p][n], a, b[2 * s], b[2 * s + 1]);
-                    }
+                for (int m = 0; m < 2; m++) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(at + 2048 * (2 * half + m) + 128 * k8 + 16 * (quad ^ (k8 & 7)));
+                    const uint32_t word[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t pair[4][4];  // [output][q]: inputs q and q + 4
+#pragma unroll
+                    for (int k = 0; k < 4; k++)
+#pragma unroll
+                        for (int q = 0; q < 4; q++)
+                            pair[k][q] = D::code_pair(word[k], q, zero[m][k]);
+#pragma unroll
+                    for (int n = 0; n < NT; n++)
+#pragma unroll
+                        for (int p = 0; p < 2; p++)
+#pragma unroll
+                            for (int q = 0; q < 2; q++) {
+                                const uint32_t a[4] = {pair[2 * p][2 * q], pair[2 * p + 1][2 * q], pair[2 * p][2 * q + 1],
+                                                       pair[2 * p + 1][2 * q + 1]};
+                                mma_16x8x16<D>(acc[2 * m + p][n], a, b[n][2 * q], b[n][2 * q + 1]);
+                            }
                 }
             }
-        }
-        const float s[4] = {half_bits(static_cast<uint16_t>(d.scales.x)), half_bits(static_cast<uint16_t>(d.scales.x >> 16)),
-                            half_bits(static_cast<uint16_t>(d.scales.y)), half_bits(static_cast<uint16_t>(d.scales.y >> 16))};
 #pragma unroll
-        for (int p = 0; p < 2; p++)
+            for (int m = 0; m < 2; m++) {
+                const uint2 v = *reinterpret_cast<const uint2 *>(at + kFewWords + 2 * (64 * half + 32 * m + 4 * quad));
+                const float s[4] = {half_bits(static_cast<uint16_t>(v.x)), half_bits(static_cast<uint16_t>(v.x >> 16)),
+                                    half_bits(static_cast<uint16_t>(v.y)), half_bits(static_cast<uint16_t>(v.y >> 16))};
+#pragma unroll
+                for (int p = 0; p < 2; p++)
+#pragma unroll
+                    for (int n = 0; n < NT; n++)
+#pragma unroll
+                        for (int k = 0; k < 4; k++)
+                            total[2 * m + p][n][k] = fmaf(s[2 * p + (k >> 1)], acc[2 * m + p][n][k], total[2 * m + p][n][k]);
+            }
+            __syncwarp();
+            if (lane == 0)
+                tc::barrier_arrive(empty(slot));
+            slot += kFewSets;
+            if (slot >= S::kStages) {
+                slot -= S::kStages;
+                parity ^= 1;
+            }
+        }
+    }
+    __syncthreads();  // every copy has landed and been read: the ring becomes the sets' sums
+    if (*stop) {
+        tc::let_copies_land();
+        g_gave_up = 1;
+    }
+    float *sums = reinterpret_cast<float *>(shared), *cta_sums = sums + kFewSets * 8 * NT * kM;
+    if (warp < 2 * kFewSets) {
+#pragma unroll
+        for (int i = 0; i < 4; i++)
 #pragma unroll
             for (int n = 0; n < NT; n++)
 #pragma unroll
-                for (int i = 0; i < 4; i++)
-                    total[p][n][i] = fmaf(s[2 * p + (i >> 1)], acc[p][n][i], total[p][n][i]);
-    };
-
-    const int64_t step = static_cast<int64_t>(ranks) * kFewWarps;
-    int64_t g = static_cast<int64_t>(rank) * kFewWarps + warp;
-    if (g < groups) {
-        GroupData<NT> now, next;
-        load(g, now);
-        for (; g < groups; g += step) {
-            if (g + step < groups)
-                load(g + step, next);
-            multiply(now);
-            now = next;
-        }
+                for (int k = 0; k < 4; k++) {
+                    const int row = 64 * half + 32 * (i >> 1) + 4 * quad + 2 * (i & 1) + (k >> 1), t = 8 * n + 2 * c + (k & 1);
+                    sums[((warp / 2) * 8 * NT + t) * kM + row] = total[i][n][k];
+                }
     }
-#pragma unroll
-    for (int p = 0; p < 2; p++)
-#pragma unroll
-        for (int n = 0; n < NT; n++)
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-                sums[warp][(8 * n + 2 * c + (i & 1)) * kFewRows + 4 * quad + 2 * p + (i >> 1)] = total[p][n][i];
     __syncthreads();
-#pragma unroll
-    for (int n = 0; n < NT; n++) {
-        const int e = threadIdx.x + n * 32 * kFewWarps;
+    for (int e = threadIdx.x; e < T * kM; e += kFewThreads) {
         float s = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kFewWarps; i++)
-            s += sums[i][e];
+        for (int i = 0; i < kFewSets; i++)
+            s += sums[i * 8 * NT * kM + e];
         cta_sums[e] = s;
     }
     if (ranks > 1)
         cluster.sync();
     else
         __syncthreads();
-    const int share = 8 * NT * kFewRows / ranks;
-    if (static_cast<int>(threadIdx.x) < share || NT > 1) {
-        for (int i = threadIdx.x; i < share; i += 32 * kFewWarps) {
-            const int e = rank * share + i, t = e / kFewRows;
-            const int64_t out = r0 + e % kFewRows;
-            float z[1] = {0.0f};
-            for (int k = 0; k < ranks; k++)
-                z[0] += ranks > 1 ? cluster.map_shared_rank(cta_sums, k)[e] : cta_sums[e];
-            if (t >= T || out >= w.R)
-                continue;
-            z[0] += ep.bias ? D::to_float(ep.bias[out]) : 0.0f;
-            if (ep.pre)
-                ep.pre[t * ep.ldpre + out] = D::from_float(z[0]);
-            activate(z, ep.act);
-            if (ep.res)
-                z[0] += D::to_float(ep.res[t * ep.ldres + out]);
-            ep.y[t * ep.ldy + out] = D::from_float(z[0]);
-        }
+    for (int e = rank * kFewThreads + threadIdx.x; e < T * kM; e += ranks * kFewThreads) {
+        const int t = e / kM;
+        const int64_t r = r0 + e % kM;
+        float parts[8];
+#pragma unroll
+        for (int k = 0; k < 8; k++)  // all on their way at once
+            parts[k] = k < ranks ? (ranks > 1 ? cluster.map_shared_rank(cta_sums, k)[e] : cta_sums[e]) : 0.0f;
+        float z[1] = {0.0f};
+#pragma unroll
+        for (int k = 0; k < 8; k++)
+            z[0] += parts[k];
+        if (r >= w.R)
+            continue;
+        z[0] += ep.bias ? D::to_float(ep.bias[r]) : 0.0f;
+        if (ep.pre)
+            ep.pre[t * ep.ldpre + r] = D::from_float(z[0]);
+        activate(z, ep.act);
+        if (ep.res)
+            z[0] += D::to_float(ep.res[t * ep.ldres + r]);
+        ep.y[t * ep.ldy + r] = D::from_float(z[0]);
     }
     if (ranks > 1)
         cluster.sync();  // peers keep their shared memory until it has been read
@@ -857,7 +985,8 @@ cq_status run_product(const uint16_t *act, int64_t ld, int64_t T, const Layer &w
     CUtensorMap act_map, word_map;
     const int64_t rows = kGradient ? w.K : w.R;
     if (!tc::make_map(&act_map, map_type<D>(), 2, act, T, kGradient ? w.R : w.K, ld, N, kChunk, true) ||
-        !tc::make_map(&word_map, CU_TENSOR_MAP_DATA_TYPE_INT32, 4, w.qweight, w.K / 8, w.R, w.R, kWordsPerGroup, kM, false))
+        !tc::make_map(&word_map, CU_TENSOR_MAP_DATA_TYPE_INT32, 4, w.qweight, w.K / 8, w.R, w.R, kGradient ? kWordsPerGroup : kChunk / 8,
+                      kGradient ? kChunk : kM, false))
         return CQ_ERR_CUDA;
     auto kernel = weights_product_kernel<D, N, kGradient>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Stages<N>::kBytes) != cudaSuccess)
@@ -888,17 +1017,31 @@ cq_status product(const uint16_t *act, int64_t ld, int64_t T, const Layer &w, co
                          : run_product<D, 32, kGradient>(act, ld, T, w, ep, stream);
 }
 
-// CTAs per cluster: enough warps to keep the memory busy, at least one group for each.
+// CTAs per cluster: the least number of groups in a row on an SM, a CTA costing about eight groups more
+// to start and to end.
 template <class D, int NT>
 cq_status few_rows(const uint16_t *x, int64_t ldx, int64_t T, const Layer &w, const Epilogue &ep, cudaStream_t stream)
 {
-    const int64_t tiles = (w.R + kFewRows - 1) / kFewRows, groups = w.K / kGroup, sms = sm_count();
+    const int64_t tiles = (w.R + kM - 1) / kM, groups = w.K / kGroup, sms = sm_count();
     int ranks = 1;
-    while (ranks < 8 && tiles * ranks * 2 <= 4 * sms && ranks * 2 * kFewWarps <= groups)
-        ranks *= 2;
+    int64_t least = INT64_MAX;
+    for (int n = 1; n <= 8 && n <= groups; n *= 2) {
+        const int64_t cost = (tiles * n + sms - 1) / sms * ((groups + n - 1) / n + 8);
+        if (cost < least) {
+            least = cost;
+            ranks = n;
+        }
+    }
+    CUtensorMap word_map;
+    if (!tc::make_map(&word_map, CU_TENSOR_MAP_DATA_TYPE_INT32, 4, w.qweight, w.K / 8, w.R, w.R, kWordsPerGroup, 32, true))
+        return CQ_ERR_CUDA;
+    auto kernel = few_rows_kernel<D, NT>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, FewStages<NT>::kBytes) != cudaSuccess)
+        return CQ_ERR_CUDA;
     cudaLaunchConfig_t config = {};
     config.gridDim = dim3(static_cast<unsigned>(tiles * ranks));
-    config.blockDim = dim3(32 * kFewWarps);
+    config.blockDim = dim3(kFewThreads);
+    config.dynamicSmemBytes = FewStages<NT>::kBytes;
     config.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -906,7 +1049,7 @@ cq_status few_rows(const uint16_t *x, int64_t ldx, int64_t T, const Layer &w, co
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     config.attrs = attr;
     config.numAttrs = 1;
-    return cudaLaunchKernelEx(&config, few_rows_kernel<D, NT>, x, ldx, static_cast<int>(T), w, ep) == cudaSuccess ? CQ_OK : CQ_ERR_CUDA;
+    return cudaLaunchKernelEx(&config, kernel, word_map, x, ldx, static_cast<int>(T), w, ep) == cudaSuccess ? CQ_OK : CQ_ERR_CUDA;
 }
 
 template <class D>

@@ -26,6 +26,11 @@ struct BF16 {
         const pair d = __hsub2(reinterpret_cast<const pair &>(a), reinterpret_cast<const pair &>(b));
         return reinterpret_cast<const uint32_t &>(d);
     }
+    // u - z - 1 of codes q and q + 4 of a word; zero as zero_pair gives it.
+    static __device__ __forceinline__ uint32_t code_pair(uint32_t word, int q, uint32_t zero)
+    {
+        return sub(((word >> (4 * q)) & 0x000F000Fu) | kMagic, zero);
+    }
     static __device__ __forceinline__ float to_float(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
     static __device__ __forceinline__ uint16_t from_float(float f) { return __bfloat16_as_ushort(__float2bfloat16_rn(f)); }
     static __device__ __forceinline__ uint32_t from_floats(float lo, float hi)
@@ -41,6 +46,18 @@ struct FP16 {
     static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b)
     {
         const pair d = __hsub2(reinterpret_cast<const pair &>(a), reinterpret_cast<const pair &>(b));
+        return reinterpret_cast<const uint32_t &>(d);
+    }
+    // u - z - 1 of codes q and q + 4 of a word; zero as zero_pair gives it.  Ten mantissa bits hold an
+    // odd code where it stands, as 1024 + 16 u; a sixteenth of that less 64 + z + 1 is exact, and a shift is saved.
+    static __device__ __forceinline__ uint32_t code_pair(uint32_t word, int q, uint32_t zero)
+    {
+        const uint32_t w = word >> (8 * (q / 2));
+        if (q % 2 == 0)
+            return sub((w & 0x000F000Fu) | kMagic, zero);
+        const uint32_t v = (w & 0x00F000F0u) | kMagic;
+        const pair offset = __hsub2(__float2half2_rn(960.0f), reinterpret_cast<const pair &>(zero));
+        const pair d = __hfma2(reinterpret_cast<const pair &>(v), __float2half2_rn(0.0625f), offset);
         return reinterpret_cast<const uint32_t &>(d);
     }
     static __device__ __forceinline__ float to_float(uint16_t b) { return __half2float(__ushort_as_half(b)); }
