@@ -14,6 +14,7 @@ struct Layer {
     const uint32_t *qzeros;    // [K/128][R/8]
     const uint16_t *scales;    // [K/128][R]
     int64_t R, K;
+    uint32_t low;              // kLow
 };
 
 // ---- tensor-core products with the weights ------------------------------------------------
@@ -72,12 +73,12 @@ struct Unpack;
 
 // n = u - z - 1 of the word's eight codes: pairs of adjacent inputs.
 template <class D>
-__device__ __forceinline__ void unpack_codes(uint32_t w, uint32_t zero, uint32_t (&n)[4])
+__device__ __forceinline__ void unpack_codes(uint32_t w, uint32_t zero, uint32_t low, uint32_t (&n)[4])
 {
     const uint32_t high = w >> 4;  // byte j of w starts with code 2j, byte j of this with code 2j + 1
 #pragma unroll
     for (int j = 0; j < 4; j++)
-        n[j] = D::sub((__byte_perm(w, high, j | (4 + j) << 8) & 0x000F000Fu) | D::kMagic, zero);
+        n[j] = D::sub((__byte_perm(w, high, j | (4 + j) << 8) & low) | D::kMagic, zero);
 }
 
 // fp16: the packed product rounds once.
@@ -89,10 +90,10 @@ struct Unpack<FP16> {
         : zero(zero_pair<FP16>(nibble)), s(__half2half2(__ushort_as_half(scale)))
     {
     }
-    __device__ __forceinline__ uint4 operator()(uint32_t w) const
+    __device__ __forceinline__ uint4 operator()(uint32_t w, uint32_t low) const
     {
         uint32_t n[4];
-        unpack_codes<FP16>(w, zero, n);
+        unpack_codes<FP16>(w, zero, low, n);
 #pragma unroll
         for (int j = 0; j < 4; j++) {
             const __half2 p = __hmul2(reinterpret_cast<const __half2 &>(n[j]), s);
@@ -115,10 +116,10 @@ struct Unpack<BF16> {
         hi = __bfloat162bfloat162(h);
         lo = __bfloat162bfloat162(__float2bfloat16_rn(s - __bfloat162float(h)));
     }
-    __device__ __forceinline__ uint4 operator()(uint32_t w) const
+    __device__ __forceinline__ uint4 operator()(uint32_t w, uint32_t low) const
     {
         uint32_t n[4];
-        unpack_codes<BF16>(w, zero, n);
+        unpack_codes<BF16>(w, zero, low, n);
 #pragma unroll
         for (int j = 0; j < 4; j++) {
             const __nv_bfloat162 v = reinterpret_cast<const __nv_bfloat162 &>(n[j]);
@@ -314,7 +315,7 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
             uint4 values[kSetWords];
 #pragma unroll
             for (int j = 0; j < kSetWords; j++)
-                values[j] = unpack(word[j]);
+                values[j] = unpack(word[j], w.low);
             if (!tc::barrier_wait_warp(empty(op.slot), op.parity ^ 1, stop))
                 break;
             char *to = shared + (a_at(op.slot) - base) + a;
@@ -630,7 +631,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                     for (int k = 0; k < 4; k++)
 #pragma unroll
                         for (int q = 0; q < 4; q++)
-                            pair[k][q] = D::code_pair(word[k], q, zero[m][k]);
+                            pair[k][q] = D::code_pair(word[k], q, zero[m][k], w.low);
 #pragma unroll
                     for (int n = 0; n < NT; n++)
 #pragma unroll
@@ -1101,7 +1102,7 @@ cq_status cq_w4_linear(const void *x, int64_t ldx, int dtype, int64_t T, const i
     if (!good_rows(x, ldx, K) || !good_rows(y, ldy, R) || (residual && !good_rows(residual, ldres, R)) ||
         (pre && !good_rows(pre, ldpre, R)) || (bias && !is_aligned(bias, 2)))
         return CQ_ERR_INVALID_ARG;
-    const Layer w = {reinterpret_cast<const uint32_t *>(qweight), reinterpret_cast<const uint32_t *>(qzeros), gptq_scales, R, K};
+    const Layer w = {reinterpret_cast<const uint32_t *>(qweight), reinterpret_cast<const uint32_t *>(qzeros), gptq_scales, R, K, kLow};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const uint16_t *in = static_cast<const uint16_t *>(x);
     const Epilogue ep = {static_cast<const uint16_t *>(bias), static_cast<const uint16_t *>(residual),
@@ -1120,7 +1121,7 @@ cq_status cq_w4_linear_backward(const void *dz, int64_t lddz, const void *x, int
                                                (dscales && R > 0 && !good_rows(x, ldx, K)))))
         return CQ_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const Layer w = {reinterpret_cast<const uint32_t *>(qweight), reinterpret_cast<const uint32_t *>(qzeros), gptq_scales, R, K};
+    const Layer w = {reinterpret_cast<const uint32_t *>(qweight), reinterpret_cast<const uint32_t *>(qzeros), gptq_scales, R, K, kLow};
     const uint16_t *d = static_cast<const uint16_t *>(dz), *xs = static_cast<const uint16_t *>(x);
     if (dx && T > 0) {
         if (R == 0)

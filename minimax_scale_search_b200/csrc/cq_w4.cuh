@@ -15,6 +15,11 @@ namespace cq {
 constexpr int kGroup = 128;       // inputs per scale
 constexpr int kWordsPerGroup = 16;
 
+// Masks a code in each half of a register.  Kernels get it as an argument: with both the mask and the
+// magic number known, (x & mask) | magic becomes two instructions with an immediate each; from
+// a register it is one (one row of the 37,888 x 8,192 layer: 45 us with two).
+constexpr uint32_t kLow = 0x000F000Fu;
+
 // One 16-bit element type: packed integers, conversions, packed arithmetic.
 // magic | u, u < 16, is the value 2^p + u of the type (p its mantissa bits), so
 // subtracting 2^p + z + 1 leaves u - (z + 1) exactly.
@@ -26,10 +31,10 @@ struct BF16 {
         const pair d = __hsub2(reinterpret_cast<const pair &>(a), reinterpret_cast<const pair &>(b));
         return reinterpret_cast<const uint32_t &>(d);
     }
-    // u - z - 1 of codes q and q + 4 of a word; zero as zero_pair gives it.
-    static __device__ __forceinline__ uint32_t code_pair(uint32_t word, int q, uint32_t zero)
+    // u - z - 1 of codes q and q + 4 of a word; zero as zero_pair gives it, low is kLow.
+    static __device__ __forceinline__ uint32_t code_pair(uint32_t word, int q, uint32_t zero, uint32_t low)
     {
-        return sub(((word >> (4 * q)) & 0x000F000Fu) | kMagic, zero);
+        return sub(((word >> (4 * q)) & low) | kMagic, zero);
     }
     static __device__ __forceinline__ float to_float(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
     static __device__ __forceinline__ uint16_t from_float(float f) { return __bfloat16_as_ushort(__float2bfloat16_rn(f)); }
@@ -48,14 +53,14 @@ struct FP16 {
         const pair d = __hsub2(reinterpret_cast<const pair &>(a), reinterpret_cast<const pair &>(b));
         return reinterpret_cast<const uint32_t &>(d);
     }
-    // u - z - 1 of codes q and q + 4 of a word; zero as zero_pair gives it.  Ten mantissa bits hold an
+    // u - z - 1 of codes q and q + 4 of a word; zero as zero_pair gives it, low is kLow.  Ten mantissa bits hold an
     // odd code where it stands, as 1024 + 16 u; a sixteenth of that less 64 + z + 1 is exact, and a shift is saved.
-    static __device__ __forceinline__ uint32_t code_pair(uint32_t word, int q, uint32_t zero)
+    static __device__ __forceinline__ uint32_t code_pair(uint32_t word, int q, uint32_t zero, uint32_t low)
     {
         const uint32_t w = word >> (8 * (q / 2));
         if (q % 2 == 0)
-            return sub((w & 0x000F000Fu) | kMagic, zero);
-        const uint32_t v = (w & 0x00F000F0u) | kMagic;
+            return sub((w & low) | kMagic, zero);
+        const uint32_t v = (w & (low << 4)) | kMagic;
         const pair offset = __hsub2(__float2half2_rn(960.0f), reinterpret_cast<const pair &>(zero));
         const pair d = __hfma2(reinterpret_cast<const pair &>(v), __float2half2_rn(0.0625f), offset);
         return reinterpret_cast<const uint32_t &>(d);
