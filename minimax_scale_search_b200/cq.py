@@ -519,11 +519,15 @@ class W4Weights:
     R: int
     K: int
 
+    def _arguments(self):
+        return self.qweight.data_ptr(), self.qzeros.data_ptr(), self.scales.data_ptr(), self.R, self.K
+
 
 def w4_weights(t: GPTQTensors) -> W4Weights:
     """Checks GPTQ v1 tensors once, for w4_linear and w4_linear_backward: shapes,
     types, devices, and that g_idx is i // 128 (read to the host here; an
-    act-order layer raises ValueError)."""
+    act-order layer raises ValueError).  The result keeps the tensors and refers
+    to their memory: values written into them later are the layer's."""
     import torch
     if t.qweight.dim() != 2:
         raise ValueError("qweight must be [K/8, R]")
@@ -543,41 +547,50 @@ def w4_weights(t: GPTQTensors) -> W4Weights:
     return W4Weights(t.qweight, t.qzeros, t.scales, R, K)
 
 
-class _On:
-    """Device and stream of one call: `dev` current, outputs allocated on `stream`."""
+def _place(dev, stream):
+    """(stream handle, context) of a call on tensors of `dev`: the context makes
+    the device and the stream current, so that outputs come from the stream's
+    memory; None where they are already."""
+    import torch
+    if stream is None:
+        if torch._C._cuda_getDevice() == dev.index:
+            return torch._C._cuda_getCurrentRawStream(dev.index), None
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device != dev:
+        raise ValueError("stream belongs to another device than the tensors")
+    return stream.cuda_stream, torch.cuda.stream(stream)
 
-    def __init__(self, dev, stream):
-        import torch
-        if stream is not None and stream.device != dev:
-            raise ValueError("stream belongs to another device than the tensors")
-        self.stream = torch.cuda.current_stream(dev) if stream is None else stream
-        self.context = None
-        if stream is not None or dev.index != torch.cuda.current_device():
-            self.context = torch.cuda.stream(self.stream)
 
-    def __enter__(self):
-        if self.context is not None:
-            self.context.__enter__()
-        return ctypes.c_void_p(self.stream.cuda_stream)
+def _empty(context, shape, dtype, dev):
+    import torch
+    if context is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with context:
+        return torch.empty(shape, dtype=dtype, device=dev)
 
-    def __exit__(self, *exc):
-        if self.context is not None:
-            self.context.__exit__(*exc)
-        return False
+
+def _call(context, function, *args):
+    if context is None:
+        status = function(*args)
+    else:
+        with context:
+            status = function(*args)
+    if status != CQ_OK:
+        raise CQError(status, function.__name__)
 
 
 def _rows16(name, t, rows, cols, like):
     """Checks a [rows, cols] operand whose rows may be strided; returns its row stride."""
-    if tuple(t.shape) != (rows, cols):
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
     if t.dtype != like.dtype or t.device != like.device:
         raise ValueError(f"{name} must be {like.dtype} on {like.device}")
     if rows == 0 or cols == 0:
         return cols
-    ld = t.stride(0) if rows > 1 else max(t.stride(0), cols)
-    if rows == 1 and ld % 8:
-        ld = cols
-    if (cols > 1 and t.stride(1) != 1) or ld < cols or ld % 8 or t.data_ptr() % 16:
+    ld, inner = t.stride()
+    if rows == 1 and (ld < cols or ld % 8):
+        ld = cols  # one row: its stride does not matter
+    if inner != 1 or ld < cols or ld % 8 or t.data_ptr() % 16:
         raise ValueError(f"{name} must have contiguous rows that start on 16-byte boundaries")
     return ld
 
@@ -602,6 +615,15 @@ def _check_same_device(w, t):
         raise ValueError("the weights are on another device than the activations")
 
 
+def _overlap(a, b):
+    """Whether two operands' memory may overlap."""
+    if a.numel() == 0 or b.numel() == 0:
+        return False
+    span = lambda t: sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1  # noqa: E731
+    a0, b0 = a.data_ptr(), b.data_ptr()
+    return a0 < b0 + span(b) * b.element_size() and b0 < a0 + span(a) * a.element_size()
+
+
 def w4_linear(x, w: W4Weights, *, bias=None, activation: str = "none", residual=None, want_pre: bool = False,
               stream=None, out=None, pre=None):
     """y = activation(x W^T + bias) + residual, W the layer's 4-bit weights.
@@ -611,24 +633,34 @@ def w4_linear(x, w: W4Weights, *, bias=None, activation: str = "none", residual=
        the residual itself.  activation: one of ACTIVATIONS.
        Returns y [T, R], or (y, pre) with ``want_pre``: pre = x W^T + bias, which
        activation_backward takes."""
-    import torch
     dt, act = _dtype16("x", x), _activation(activation)
     _check_same_device(w, x)
     T, R, K = x.shape[0], w.R, w.K
     ldx = _rows16("x", x, T, K, x)
-    if bias is not None and (tuple(bias.shape) != (R,) or bias.dtype != x.dtype or bias.device != x.device or
+    if bias is not None and (bias.shape != (R,) or bias.dtype != x.dtype or bias.device != x.device or
                              not bias.is_contiguous()):
         raise ValueError(f"bias must be a contiguous {x.dtype} [{R}] tensor on {x.device}")
     ldres = _rows16("residual", residual, T, R, x) if residual is not None else 0
-    with _On(x.device, stream) as handle:
-        if out is None:
-            out = torch.empty((T, R), dtype=x.dtype, device=x.device)
-        if want_pre and pre is None:
-            pre = torch.empty((T, R), dtype=x.dtype, device=x.device)
+    handle, context = _place(x.device, stream)
+    if out is None:
+        out, ldy = _empty(context, (T, R), x.dtype, x.device), R
+    else:
         ldy = _rows16("out", out, T, R, x)
-        ldpre = _rows16("pre", pre, T, R, x) if pre is not None else 0
-        _check(lib.cq_w4_linear(_ptr(x), ldx, dt, T, _ptr(w.qweight), _ptr(w.qzeros), _ptr(w.scales), R, K, _ptr(bias),
-                                act, _ptr(residual), ldres, _ptr(out), ldy, _ptr(pre), ldpre, handle), "cq_w4_linear")
+        if _overlap(out, x):
+            raise ValueError("out must not overlap x")
+    ldpre = 0
+    if want_pre:
+        if pre is None:
+            pre, ldpre = _empty(context, (T, R), x.dtype, x.device), R
+        else:
+            ldpre = _rows16("pre", pre, T, R, x)
+            if _overlap(pre, x) or _overlap(pre, out) or (residual is not None and _overlap(pre, residual)):
+                raise ValueError("pre must not overlap another operand")
+    elif pre is not None:
+        raise ValueError("pre is written only with want_pre")
+    _call(context, lib.cq_w4_linear, x.data_ptr(), ldx, dt, T, *w._arguments(), None if bias is None else bias.data_ptr(), act,
+          None if residual is None else residual.data_ptr(), ldres, out.data_ptr(), ldy,
+          pre.data_ptr() if want_pre else None, ldpre, handle)
     return (out, pre) if want_pre else out
 
 
@@ -642,49 +674,57 @@ def w4_linear_backward(dz, x, w: W4Weights, *, want_dx: bool = True, want_dscale
     _check_same_device(w, dz)
     T, R, K = dz.shape[0], w.R, w.K
     lddz = _rows16("dz", dz, T, R, dz)
-    ldx = _rows16("x", x, T, K, dz) if want_dscales else 0
-    if dscales is not None and (tuple(dscales.shape) != (K // GROUP, R) or dscales.dtype != torch.float32 or
-                                dscales.device != dz.device or not dscales.is_contiguous()):
-        raise ValueError(f"dscales must be contiguous float32 [{K // GROUP}, {R}]")
-    with _On(dz.device, stream) as handle:
-        if want_dx and dx is None:
-            dx = torch.empty((T, K), dtype=dz.dtype, device=dz.device)
-        if want_dscales and dscales is None:
-            dscales = torch.empty((K // GROUP, R), dtype=torch.float32, device=dz.device)
-        if not want_dx:
-            dx = None
-        if not want_dscales:
-            x = dscales = None
-        lddx = _rows16("dx", dx, T, K, dz) if dx is not None else 0
-        _check(lib.cq_w4_linear_backward(_ptr(dz), lddz, _ptr(x), ldx, dt, T, _ptr(w.qweight), _ptr(w.qzeros),
-                                         _ptr(w.scales), R, K, _ptr(dx), lddx, _ptr(dscales), handle),
-               "cq_w4_linear_backward")
+    handle, context = _place(dz.device, stream)
+    ldx = lddx = 0
+    if not want_dx:
+        dx = None
+    elif dx is None:
+        dx, lddx = _empty(context, (T, K), dz.dtype, dz.device), K
+    else:
+        lddx = _rows16("dx", dx, T, K, dz)
+        if _overlap(dx, dz) or (want_dscales and _overlap(dx, x)):
+            raise ValueError("dx must not overlap dz or x")
+    if not want_dscales:
+        x = dscales = None
+    else:
+        ldx = _rows16("x", x, T, K, dz)
+        if dscales is None:
+            dscales = _empty(context, (K // GROUP, R), torch.float32, dz.device)
+        elif (dscales.shape != (K // GROUP, R) or dscales.dtype != torch.float32 or dscales.device != dz.device or
+              not dscales.is_contiguous() or dscales.data_ptr() % 16):
+            raise ValueError(f"dscales must be contiguous 16-byte aligned float32 [{K // GROUP}, {R}]")
+    _call(context, lib.cq_w4_linear_backward, dz.data_ptr(), lddz, None if x is None else x.data_ptr(), ldx, dt, T,
+          *w._arguments(), None if dx is None else dx.data_ptr(), lddx, None if dscales is None else dscales.data_ptr(), handle)
     return dx, dscales
 
 
 def activation_backward(dy, pre, activation: str, *, want_dbias: bool = True, stream=None, out=None, dbias=None):
     """(dz, dbias) from the gradient dy at act(pre) + residual: dz = dy act'(pre) in
     dy's type, dbias its column sums (float32 [R], taken before that rounding)
-    or None.  dy, pre: [T, R] bfloat16 or float16; R a multiple of 8."""
+    or None.  dy, pre: [T, R] bfloat16 or float16; R a multiple of 8.  ``out`` may
+    be dy or pre itself."""
     import torch
     dt, act = _dtype16("dy", dy), _activation(activation)
     T, R = dy.shape
     if R % 8:
         raise ValueError("R must be a multiple of 8")
     lddy, ldpre = _rows16("dy", dy, T, R, dy), _rows16("pre", pre, T, R, dy)
-    if dbias is not None and (tuple(dbias.shape) != (R,) or dbias.dtype != torch.float32 or dbias.device != dy.device or
-                              not dbias.is_contiguous()):
-        raise ValueError(f"dbias must be contiguous float32 [{R}]")
-    with _On(dy.device, stream) as handle:
-        if out is None:
-            out = torch.empty((T, R), dtype=dy.dtype, device=dy.device)
-        if want_dbias and dbias is None:
-            dbias = torch.empty(R, dtype=torch.float32, device=dy.device)
-        if not want_dbias:
-            dbias = None
+    handle, context = _place(dy.device, stream)
+    if out is None:
+        out, lddz = _empty(context, (T, R), dy.dtype, dy.device), R
+    else:
         lddz = _rows16("out", out, T, R, dy)
-        _check(lib.cq_activation_backward(_ptr(dy), lddy, _ptr(pre), ldpre, dt, T, R, act, _ptr(out), lddz, _ptr(dbias),
-                                          handle), "cq_activation_backward")
+        for t, ld in ((dy, lddy), (pre, ldpre)):
+            if _overlap(out, t) and (out.data_ptr() != t.data_ptr() or lddz != ld):
+                raise ValueError("out must be dy or pre itself, or not overlap them")
+    if not want_dbias:
+        dbias = None
+    elif dbias is None:
+        dbias = _empty(context, (R,), torch.float32, dy.device)
+    elif dbias.shape != (R,) or dbias.dtype != torch.float32 or dbias.device != dy.device or not dbias.is_contiguous():
+        raise ValueError(f"dbias must be contiguous float32 [{R}]")
+    _call(context, lib.cq_activation_backward, dy.data_ptr(), lddy, pre.data_ptr(), ldpre, dt, T, R, act, out.data_ptr(),
+          lddz, None if dbias is None else dbias.data_ptr(), handle)
     return out, dbias
 
 
@@ -700,6 +740,17 @@ def _table(ids, codes, K):
     return ids.numel(), codes.numel() // (K // 8)
 
 
+def _float_type(name, dtype):
+    import torch
+    if dtype is torch.bfloat16:
+        return DTYPE_BF16
+    if dtype is torch.float16:
+        return DTYPE_FP16
+    if dtype is torch.float32:
+        return DTYPE_FP32
+    raise ValueError(f"{name} must be bfloat16, float16 or float32")
+
+
 def w4_embedding(ids, scales, codes, K: int, *, multiplier: float = 1.0, dtype=None, stream=None, out=None):
     """Rows ids of a [V, K] table quantised by select_scales (scales [V*K/128],
     codes [V*K/128, 16]): multiplier * scale * q, rounded once to ``dtype`` (float16
@@ -711,21 +762,17 @@ def w4_embedding(ids, scales, codes, K: int, *, multiplier: float = 1.0, dtype=N
     if scales.element_size() != 2 or scales.numel() != V * (K // GROUP) or scales.device != ids.device or \
             not scales.is_contiguous():
         raise ValueError("scales must hold V*K/128 contiguous 16-bit patterns on the device of ids")
-    if out is not None:
-        dtype = out.dtype if dtype is None else dtype
-    dtype = torch.float16 if dtype is None else dtype
-    dt = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_FP16, torch.float32: DTYPE_FP32}.get(dtype)
-    if dt is None:
-        raise ValueError("dtype must be bfloat16, float16 or float32")
-    shape = tuple(ids.shape) + (K,)
-    if out is not None and (tuple(out.shape) != shape or out.dtype != dtype or out.device != ids.device or
-                            not out.is_contiguous()):
+    if dtype is None:
+        dtype = torch.float16 if out is None else out.dtype
+    dt = _float_type("dtype", dtype)
+    shape = (*ids.shape, K)
+    handle, context = _place(ids.device, stream)
+    if out is None:
+        out = _empty(context, shape, dtype, ids.device)
+    elif out.shape != shape or out.dtype != dtype or out.device != ids.device or not out.is_contiguous():
         raise ValueError(f"out must be contiguous {dtype} {list(shape)}")
-    with _On(ids.device, stream) as handle:
-        if out is None:
-            out = torch.empty(shape, dtype=dtype, device=ids.device)
-        _check(lib.cq_w4_embedding(_ptr(ids), int(ids.dtype == torch.int64), T, _ptr(scales), _ptr(codes), V, K,
-                                   float(multiplier), dt, _ptr(out), handle), "cq_w4_embedding")
+    _call(context, lib.cq_w4_embedding, ids.data_ptr(), int(ids.dtype is torch.int64), T, scales.data_ptr(), codes.data_ptr(),
+          V, K, multiplier, dt, out.data_ptr(), handle)
     return out
 
 
@@ -737,35 +784,30 @@ def w4_embedding_backward(dout, ids, codes, *, multiplier: float = 1.0, stream=N
     """Gradient of a quantised table's group scales: float32 [V, K/128], zero for
     the rows that no id names.  dout: [*ids.shape, K] bfloat16, float16 or
     float32; ids outside [0, V) have no gradient.  ``workspace``: uint8, at least
-    w4_embedding_workspace_bytes(T, K); calls that share one must be ordered on
-    one stream."""
+    w4_embedding_workspace_bytes(T, K) and 256-byte aligned; calls that share one
+    must be ordered on one stream."""
     import torch
-    if not dout.is_cuda or dout.dim() < 1 or not dout.is_contiguous() or tuple(dout.shape[:-1]) != tuple(ids.shape):
+    if not dout.is_cuda or dout.dim() < 1 or not dout.is_contiguous() or dout.shape[:-1] != ids.shape:
         raise ValueError("dout must be a contiguous CUDA tensor [*ids.shape, K]")
-    dt = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_FP16, torch.float32: DTYPE_FP32}.get(dout.dtype)
-    if dt is None:
-        raise ValueError("dout must be bfloat16, float16 or float32")
+    dt = _float_type("dout", dout.dtype)
     K = dout.shape[-1]
     T, V = _table(ids, codes, K)
     if dout.device != ids.device:
         raise ValueError("dout must be on the device of ids")
-    if out is not None and (tuple(out.shape) != (V, K // GROUP) or out.dtype != torch.float32 or
-                            out.device != ids.device or not out.is_contiguous()):
-        raise ValueError(f"out must be contiguous float32 [{V}, {K // GROUP}]")
     wsb = w4_embedding_workspace_bytes(T, K)
     if workspace is not None and (workspace.device != ids.device or not workspace.is_contiguous() or
                                   workspace.numel() * workspace.element_size() < wsb):
         raise ValueError(f"workspace must hold {wsb} contiguous bytes on the device of ids")
-    with _On(ids.device, stream) as handle:
-        if out is None:
-            out = torch.empty((V, K // GROUP), dtype=torch.float32, device=ids.device)
-        if workspace is None:
-            workspace = torch.empty(wsb, dtype=torch.uint8, device=ids.device)
-        _check(lib.cq_w4_embedding_backward(_ptr(dout), dt, _ptr(ids), int(ids.dtype == torch.int64), T, _ptr(codes), V, K,
-                                            float(multiplier), _ptr(out), _ptr(workspace), wsb, handle),
-               "cq_w4_embedding_backward")
+    handle, context = _place(ids.device, stream)
+    if out is None:
+        out = _empty(context, (V, K // GROUP), torch.float32, ids.device)
+    elif out.shape != (V, K // GROUP) or out.dtype != torch.float32 or out.device != ids.device or not out.is_contiguous():
+        raise ValueError(f"out must be contiguous float32 [{V}, {K // GROUP}]")
+    if workspace is None:
+        workspace = _empty(context, (wsb,), torch.uint8, ids.device)
+    _call(context, lib.cq_w4_embedding_backward, dout.data_ptr(), dt, ids.data_ptr(), int(ids.dtype is torch.int64), T,
+          codes.data_ptr(), V, K, multiplier, out.data_ptr(), workspace.data_ptr(), wsb, handle)
     return out
-
 
 
 def read_counters(workspace, stream=None) -> dict:

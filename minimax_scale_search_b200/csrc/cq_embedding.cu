@@ -2,24 +2,57 @@
 //
 // The table is the selection's own output for a [V][K] matrix: scales
 // [V * K/128] and code words [V * K/128][16], so a row's words are contiguous.
+//
+// Lookup.  out[t] = m s q of row ids[t]; the bytes of the output bound it.  A thread takes four
+// words (8 values each) 256 words apart, all their loads before the first store.
+//
+// Gradient.  dscales[v][g] = m sum_{t: ids[t] = v} sum_{i in g} dout[t][i] q[v][i], in
+// three launches:
+//  1. dots[t][g] = sum_{i in g} dout[t][i] q[id_t][i] (fp32, one pass over dout, which is what
+//     bounds the whole); the same launch fills dscales with zeros and sorts the tokens by
+//     (id, t): up to kRankMost tokens by counting, for each, the tokens before it (T^2
+//     comparisons, no further launch), above with a radix sort of its own launches;
+//  2. sums over the runs of equal ids within each chunk of 64 sorted tokens, in fp64; a run that
+//     lies inside a chunk is done, others leave a part at the chunk's head or tail;
+//  3. the runs across chunks, from their parts in order.
+// So a row that every token names is summed by many threads, and the order of the sums is fixed.
 #include "cq_w4.cuh"
 
 namespace cq {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kWordsAhead = 4;                          // words per thread in flight
+constexpr int kBlockWords = kThreads * kWordsAhead;
+constexpr int kRankMost = 16384;                        // tokens sorted by counting
+constexpr int kRankTokens = 8;                          // per warp
+constexpr int kRankTile = 1024;                         // keys in shared memory
+constexpr int kChunk = 64;                              // sorted tokens per partial sum
+constexpr int kSortTokens = 4096;                       // per CTA of the radix sort
 
 struct Ids {
     const void *p;
     int wide;  // int64 ids
     int64_t V;
-    // The row of token t, or -1 for an id outside [0, V).
-    __device__ __forceinline__ int64_t row(int64_t t) const
+    // The row of token t, or V for an id outside [0, V).
+    __device__ __forceinline__ uint32_t key(int64_t t) const
     {
         const int64_t v = wide ? static_cast<const int64_t *>(p)[t] : static_cast<const int32_t *>(p)[t];
-        return v >= 0 && v < V ? v : -1;
+        return static_cast<uint32_t>(v >= 0 && v < V ? v : V);
     }
 };
+
+// i / d and i mod d, in 32 bits where they fit.
+__device__ __forceinline__ void divide(int64_t i, int64_t d, bool narrow, int64_t &q, int64_t &r)
+{
+    if (narrow) {
+        q = static_cast<uint32_t>(i) / static_cast<uint32_t>(d);
+        r = static_cast<uint32_t>(i) - static_cast<uint32_t>(q) * static_cast<uint32_t>(d);
+    } else {
+        q = i / d;
+        r = i - q * d;
+    }
+}
 
 // Eight values from a code word: q = u - 8.
 __device__ __forceinline__ void unpack(uint32_t word, float (&q)[8])
@@ -34,130 +67,373 @@ __device__ __forceinline__ void store8(void *out, int64_t i, const float (&v)[8]
 {
     if (DT == CQ_DTYPE_FP32) {
         float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(out) + i);
-        o[0] = make_float4(v[0], v[1], v[2], v[3]);
-        o[1] = make_float4(v[4], v[5], v[6], v[7]);
+        __stcs(o, make_float4(v[0], v[1], v[2], v[3]));
+        __stcs(o + 1, make_float4(v[4], v[5], v[6], v[7]));
     } else {
-        uint32_t h[4];
-#pragma unroll
-        for (int j = 0; j < 4; j++)
-            h[j] = DT == CQ_DTYPE_BF16 ? BF16::from_floats(v[2 * j], v[2 * j + 1]) : FP16::from_floats(v[2 * j], v[2 * j + 1]);
-        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + i) = make_uint4(h[0], h[1], h[2], h[3]);
+        const uint4 h = DT == CQ_DTYPE_BF16 ? narrow<BF16>(v) : narrow<FP16>(v);
+        __stcs(reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + i), h);
     }
 }
 
+// Eight elements of dout as they lie in memory, and their values.
 template <int DT>
-__device__ __forceinline__ void load8(const void *in, int64_t i, float (&v)[8])
+struct Eight {
+    uint4 a, b;
+    __device__ __forceinline__ void load(const void *in, int64_t i)
+    {
+        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const char *>(in) + i * (DT == CQ_DTYPE_FP32 ? 4 : 2));
+        a = __ldcs(p);
+        if (DT == CQ_DTYPE_FP32)
+            b = __ldcs(p + 1);
+    }
+    __device__ __forceinline__ void values(float (&v)[8]) const
+    {
+        if (DT == CQ_DTYPE_FP32) {
+            v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y); v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
+            v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y); v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
+        } else if (DT == CQ_DTYPE_BF16) {
+            widen<BF16>(a, v);
+        } else {
+            widen<FP16>(a, v);
+        }
+    }
+};
+
+template <int DT>
+__global__ void __launch_bounds__(kThreads) embedding_kernel(Ids ids, int64_t T, const uint16_t *__restrict__ scales,
+                                                             const uint32_t *__restrict__ codes, int64_t K8, float multiplier,
+                                                             void *__restrict__ out)
 {
-    if (DT == CQ_DTYPE_FP32) {
-        const float4 a = __ldcs(reinterpret_cast<const float4 *>(static_cast<const float *>(in) + i));
-        const float4 b = __ldcs(reinterpret_cast<const float4 *>(static_cast<const float *>(in) + i) + 1);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
-        const uint4 u = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(in) + i));
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    const int64_t n = T * K8;
+    const bool narrow = n < (static_cast<int64_t>(1) << 32);
+    for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kBlockWords + threadIdx.x; i0 < n;
+         i0 += static_cast<int64_t>(gridDim.x) * kBlockWords) {
+        uint32_t word[kWordsAhead], row[kWordsAhead];
+        uint16_t scale[kWordsAhead];
+        int64_t k[kWordsAhead];
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-            const uint16_t b = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
-            v[j] = DT == CQ_DTYPE_BF16 ? BF16::to_float(b) : FP16::to_float(b);
+        for (int u = 0; u < kWordsAhead; u++) {
+            const int64_t i = i0 + u * kThreads;
+            int64_t t = 0;
+            if (i < n)
+                divide(i, K8, narrow, t, k[u]);
+            row[u] = i < n ? ids.key(t) : static_cast<uint32_t>(ids.V);
+        }
+#pragma unroll
+        for (int u = 0; u < kWordsAhead; u++)
+            if (row[u] < ids.V) {
+                word[u] = codes[row[u] * K8 + k[u]];
+                scale[u] = scales[row[u] * (K8 / kWordsPerGroup) + k[u] / kWordsPerGroup];
+            }
+#pragma unroll
+        for (int u = 0; u < kWordsAhead; u++) {
+            const int64_t i = i0 + u * kThreads;
+            if (i >= n)
+                break;
+            float q[8] = {};
+            if (row[u] < ids.V) {
+                const float s = half_bits(scale[u]);
+                unpack(word[u], q);
+#pragma unroll
+                for (int j = 0; j < 8; j++)
+                    q[j] = multiplier * (s * q[j]);
+            }
+            store8<DT>(out, i * 8, q);
         }
     }
 }
 
-// One thread per code word.
-template <int DT>
-__global__ void __launch_bounds__(kThreads) embedding_kernel(Ids ids, int64_t T, const uint16_t *scales,
-                                                             const uint32_t *codes, int64_t K8, float multiplier, void *out)
-{
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads, n = T * K8;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n; i += stride) {
-        const int64_t t = i / K8, k = i - t * K8, v = ids.row(t);
-        float q[8] = {};
-        if (v >= 0) {
-            const float s = half_bits(scales[v * (K8 / kWordsPerGroup) + k / kWordsPerGroup]);
-            unpack(codes[v * K8 + k], q);
-#pragma unroll
-            for (int j = 0; j < 8; j++)
-                q[j] = multiplier * (s * q[j]);
-        }
-        store8<DT>(out, i * 8, q);
-    }
-}
+// ---- gradient ------------------------------------------------------------------------------------
 
-// dots[t][g] = sum_{i in g} dout[t][i] q[id_t][i]: 16 lanes per group.
-template <int DT>
-__global__ void __launch_bounds__(kThreads) token_dots_kernel(const void *dout, Ids ids, int64_t T, const uint32_t *codes,
-                                                              int64_t K8, float *dots)
+// order[rank] = t, key[rank] = row: a warp counts, for eight tokens, the tokens before
+// each by (row, t).
+__device__ void rank_tokens(const Ids &ids, int T, int warps_before, uint32_t *key, int32_t *order)
 {
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads, n = T * K8;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n; i += stride) {  // n % 16 == 0
-        const int64_t t = i / K8, k = i - t * K8, v = ids.row(t);
-        float s = 0.0f;
-        if (v >= 0) {
-            float d[8], q[8];
-            load8<DT>(dout, i * 8, d);
-            unpack(codes[v * K8 + k], q);
+    __shared__ uint32_t tile[kRankTile];
+    const int lane = threadIdx.x % 32;
+    const int t0 = (warps_before + static_cast<int>(threadIdx.x) / 32) * kRankTokens;
+    uint32_t mine[kRankTokens];
+    int rank[kRankTokens] = {};
 #pragma unroll
-            for (int j = 0; j < 8; j++)
-                s = fmaf(d[j], q[j], s);
-        }
-        const unsigned mask = 0xFFFFu << (threadIdx.x & 16);
-        for (int o = 8; o > 0; o >>= 1)
-            s += __shfl_xor_sync(mask, s, o, 16);
-        if ((threadIdx.x & 15) == 0)
-            dots[i / kWordsPerGroup] = s;
-    }
-}
-
-// order[rank] = t and key[rank] = id (V for no row), rank the number of tokens that
-// come before t by (id, t).
-__global__ void __launch_bounds__(kThreads) rank_kernel(Ids ids, int64_t T, int64_t *key, int32_t *order)
-{
-    __shared__ int64_t other[kThreads];
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    int64_t mine = -1;
-    if (t < T) {
-        mine = ids.row(t);
-        mine = mine < 0 ? ids.V : mine;
-    }
-    int64_t rank = 0;
-    for (int64_t j0 = 0; j0 < T; j0 += kThreads) {
+    for (int i = 0; i < kRankTokens; i++)
+        mine[i] = t0 + i < T ? ids.key(t0 + i) : 0;
+    for (int j0 = 0; j0 < T; j0 += kRankTile) {
         __syncthreads();
-        if (j0 + threadIdx.x < T) {
-            const int64_t v = ids.row(j0 + threadIdx.x);
-            other[threadIdx.x] = v < 0 ? ids.V : v;
-        }
+        for (int j = threadIdx.x; j < kRankTile; j += kThreads)
+            tile[j] = j0 + j < T ? ids.key(j0 + j) : 0xFFFFFFFFu;
         __syncthreads();
-        const int m = static_cast<int>(T - j0 < kThreads ? T - j0 : kThreads);
-        for (int j = 0; j < m; j++)
-            rank += other[j] < mine || (other[j] == mine && j0 + j < t);
+        for (int j = lane; j < kRankTile; j += 32) {
+            const uint32_t other = tile[j];
+            const int at = j0 + j;
+            // (other, at) < (mine, t)  <=>  other < mine + (at < t); the eight t are adjacent
+            if (at - lane + 31 < t0) {
+#pragma unroll
+                for (int i = 0; i < kRankTokens; i++)
+                    rank[i] += other <= mine[i];
+            } else {
+#pragma unroll
+                for (int i = 0; i < kRankTokens; i++)
+                    rank[i] += other < mine[i] + (at < t0 + i);
+            }
+        }
     }
-    if (t < T) {
-        key[rank] = mine;
-        order[rank] = static_cast<int32_t>(t);
+#pragma unroll
+    for (int i = 0; i < kRankTokens; i++) {
+        const int r = __reduce_add_sync(0xFFFFFFFFu, rank[i]);
+        if (lane == i && t0 + i < T) {
+            key[r] = mine[i];
+            order[r] = t0 + i;
+        }
     }
 }
 
-// One thread per (first token of a run of equal ids, group): sums the run in fp64.
-__global__ void __launch_bounds__(kThreads) run_sums_kernel(const int64_t *key, const int32_t *order, int64_t T, int64_t V,
-                                                            const float *dots, int64_t ng, float multiplier, float *dscales)
+// Blocks below `rank_blocks` sort by counting; the others form the dots (16 lanes per group) and
+// write the zeros.
+template <int DT>
+__global__ void __launch_bounds__(kThreads) dots_kernel(const void *__restrict__ dout, Ids ids, int64_t T,
+                                                        const uint32_t *__restrict__ codes, int64_t K8, float *__restrict__ dots,
+                                                        int rank_blocks, uint32_t *key, int32_t *order, float *__restrict__ dscales)
 {
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    if (i >= T * ng)
+    if (static_cast<int>(blockIdx.x) < rank_blocks) {
+        rank_tokens(ids, static_cast<int>(T), blockIdx.x * (kThreads / 32), key, order);
         return;
-    const int64_t j0 = i / ng, g = i - j0 * ng, v = key[j0];
-    if (v >= V || (j0 > 0 && key[j0 - 1] == v))
-        return;
-    double s = 0.0;
-    for (int64_t j = j0; j < T && key[j] == v; j++)
-        s += dots[order[j] * ng + g];
-    dscales[v * ng + g] = static_cast<float>(s * multiplier);
+    }
+    const int64_t block = blockIdx.x - rank_blocks, blocks = gridDim.x - rank_blocks;
+    const int64_t n = T * K8;
+    const bool narrow = n < (static_cast<int64_t>(1) << 32);
+    for (int64_t b0 = block * kBlockWords; b0 < n; b0 += blocks * kBlockWords) {
+        uint32_t word[kWordsAhead];
+        Eight<DT> d[kWordsAhead];
+        bool named[kWordsAhead];
+#pragma unroll
+        for (int u = 0; u < kWordsAhead; u++) {
+            const int64_t i = b0 + u * kThreads + threadIdx.x;  // n % 16 == 0: a half-warp in or out together
+            named[u] = false;
+            if (i < n) {
+                int64_t t, k;
+                divide(i, K8, narrow, t, k);
+                const uint32_t v = ids.key(t);
+                named[u] = v < ids.V;
+                if (named[u]) {
+                    d[u].load(dout, i * 8);
+                    word[u] = codes[v * K8 + k];
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kWordsAhead; u++) {
+            const int64_t i = b0 + u * kThreads + threadIdx.x;
+            float s = 0.0f;
+            if (named[u]) {
+                float x[8], q[8];
+                d[u].values(x);
+                unpack(word[u], q);
+#pragma unroll
+                for (int j = 0; j < 8; j++)
+                    s = fmaf(x[j], q[j], s);
+            }
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1)
+                s += __shfl_xor_sync(0xFFFFFFFFu, s, o, 16);
+            if (i < n && (threadIdx.x & 15) == 0)
+                dots[i / kWordsPerGroup] = s;
+        }
+    }
+    const int64_t outputs = ids.V * (K8 / kWordsPerGroup);
+    for (int64_t i = block * kThreads + threadIdx.x; i < outputs; i += blocks * kThreads)
+        dscales[i] = 0.0f;
 }
 
-unsigned grid_for(int64_t n)
+// The parts of a run that crosses chunks: [chunk][group], what the chunk has of a run that
+// began before it (head) and of one that goes on after it (tail).
+struct Parts {
+    double *head, *tail;
+};
+
+// `width` threads (a power of two) have a chunk's groups.
+__global__ void __launch_bounds__(kThreads) chunk_sums_kernel(const uint32_t *__restrict__ key, const int32_t *__restrict__ order,
+                                                              int64_t T, int64_t V, const float *__restrict__ dots, int64_t ng,
+                                                              int width, float multiplier, Parts parts, float *__restrict__ dscales)
 {
-    const int64_t blocks = (n + kThreads - 1) / kThreads, cap = 148 * 64;
-    return static_cast<unsigned>(blocks < cap ? blocks : cap);
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * (kThreads / width) + threadIdx.x / width;
+    const int64_t p0 = c * kChunk, p1 = p0 + kChunk < T ? p0 + kChunk : T;
+    if (p0 >= T)
+        return;
+    for (int64_t g = threadIdx.x % width; g < ng; g += width) {
+        uint32_t current = key[p0];
+        bool head = p0 > 0 && key[p0 - 1] == current;
+        double sum = 0.0;
+        auto finish = [&](bool goes_on) {
+            if (current >= V)
+                return;
+            if (head)
+                parts.head[c * ng + g] = sum;
+            else if (goes_on)
+                parts.tail[c * ng + g] = sum;
+            else
+                dscales[current * ng + g] = static_cast<float>(sum * multiplier);
+        };
+        constexpr int kAhead = 8;
+        for (int64_t p = p0; p < p1; p += kAhead) {
+            uint32_t k[kAhead];
+            float d[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; u++)
+                if (p + u < p1) {
+                    k[u] = key[p + u];
+                    d[u] = dots[order[p + u] * ng + g];
+                }
+#pragma unroll
+            for (int u = 0; u < kAhead; u++)
+                if (p + u < p1) {
+                    if (k[u] != current) {
+                        finish(false);
+                        current = k[u];
+                        head = false;
+                        sum = 0.0;
+                    }
+                    sum += d[u];
+                }
+        }
+        finish(p1 < T && key[p1] == current);
+    }
+}
+
+// Runs that begin in chunk c and go on after it.
+__global__ void __launch_bounds__(kThreads) join_runs_kernel(const uint32_t *__restrict__ key, int64_t T, int64_t V, int64_t ng,
+                                                             int width, float multiplier, Parts parts, float *__restrict__ dscales)
+{
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * (kThreads / width) + threadIdx.x / width, p0 = c * kChunk;
+    if (p0 + kChunk >= T)
+        return;
+    const uint32_t v = key[p0 + kChunk];
+    if (v >= V || key[p0 + kChunk - 1] != v || (p0 > 0 && key[p0 - 1] == v))
+        return;
+    int64_t last = c + 1, beyond = (T - 1) / kChunk + 1;  // the last chunk that begins with v
+    while (beyond - last > 1) {
+        const int64_t mid = (last + beyond) / 2;
+        if (key[mid * kChunk] == v)
+            last = mid;
+        else
+            beyond = mid;
+    }
+    for (int64_t g = threadIdx.x % width; g < ng; g += width) {
+        double sum = parts.tail[c * ng + g];
+#pragma unroll 8
+        for (int64_t i = c + 1; i <= last; i++)
+            sum += parts.head[i * ng + g];
+        dscales[v * ng + g] = static_cast<float>(sum * multiplier);
+    }
+}
+
+// ---- radix sort of the tokens by row, 8 bits a pass, stable ---------------------------------------
+
+struct SortPass {
+    const uint32_t *key_in;   // null in the first pass: the tokens in their order
+    const int32_t *order_in;
+    uint32_t *key_out;
+    int32_t *order_out;
+    int32_t *counts;          // [256][blocks]
+    int shift;
+};
+
+__device__ __forceinline__ uint32_t sort_key(const Ids &ids, const SortPass &s, int64_t i)
+{
+    return s.key_in ? s.key_in[i] : ids.key(i);
+}
+
+__global__ void __launch_bounds__(kThreads) sort_count_kernel(Ids ids, int64_t T, SortPass s)
+{
+    __shared__ int32_t count[256];
+    count[threadIdx.x] = 0;
+    __syncthreads();
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kSortTokens;
+    for (int j = threadIdx.x; j < kSortTokens && i0 + j < T; j += kThreads)
+        atomicAdd(&count[(sort_key(ids, s, i0 + j) >> s.shift) & 255u], 1);
+    __syncthreads();
+    s.counts[threadIdx.x * static_cast<int64_t>(gridDim.x) + blockIdx.x] = count[threadIdx.x];
+}
+
+// counts -> the number of tokens before each (digit, block), by one CTA.
+__global__ void __launch_bounds__(1024) sort_scan_kernel(int32_t *counts, int64_t n)
+{
+    __shared__ int32_t sums[32];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    int32_t before = 0;
+    for (int64_t i0 = 0; i0 < n; i0 += 1024) {
+        const int64_t i = i0 + threadIdx.x;
+        const int32_t mine = i < n ? counts[i] : 0;
+        int32_t x = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+            x += lane >= o ? y : 0;
+        }
+        if (lane == 31)
+            sums[warp] = x;
+        __syncthreads();
+        int32_t w = sums[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t y = __shfl_up_sync(0xFFFFFFFFu, w, o);
+            w += lane >= o ? y : 0;
+        }
+        const int32_t warps_before = warp > 0 ? __shfl_sync(0xFFFFFFFFu, w, (warp + 31) % 32) : 0;
+        const int32_t total = __shfl_sync(0xFFFFFFFFu, w, 31);
+        if (i < n)
+            counts[i] = before + warps_before + x - mine;
+        before += total;
+        __syncthreads();
+    }
+}
+
+// A warp has 512 tokens in a row; first its digits' counts, then each token's place: the digit's
+// start, the warps before, the warp's tokens before.
+__global__ void __launch_bounds__(kThreads) sort_scatter_kernel(Ids ids, int64_t T, SortPass s)
+{
+    constexpr int kWarps = kThreads / 32, kPerWarp = kSortTokens / kWarps;
+    __shared__ int32_t count[kWarps][256];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    for (int j = threadIdx.x; j < kWarps * 256; j += kThreads)
+        count[j / 256][j % 256] = 0;
+    __syncthreads();
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kSortTokens + warp * kPerWarp;
+    for (int j = lane; j < kPerWarp; j += 32)
+        if (i0 + j < T)
+            atomicAdd(&count[warp][(sort_key(ids, s, i0 + j) >> s.shift) & 255u], 1);
+    __syncthreads();
+    int32_t at = s.counts[threadIdx.x * static_cast<int64_t>(gridDim.x) + blockIdx.x];
+#pragma unroll
+    for (int w = 0; w < kWarps; w++) {
+        const int32_t n = count[w][threadIdx.x];
+        count[w][threadIdx.x] = at;
+        at += n;
+    }
+    __syncthreads();
+    for (int j = lane; j < kPerWarp; j += 32) {
+        const bool inside = i0 + j < T;
+        const uint32_t k = inside ? sort_key(ids, s, i0 + j) : 0;
+        const uint32_t digit = inside ? (k >> s.shift) & 255u : 256u;
+        const unsigned same = __match_any_sync(0xFFFFFFFFu, digit);
+        const int before = __popc(same & ((1u << lane) - 1));
+        int32_t place = 0;
+        if (inside)
+            place = count[warp][digit] + before;
+        __syncwarp();
+        if (inside) {
+            if (before == 0)
+                count[warp][digit] += __popc(same);
+            s.key_out[place] = k;
+            s.order_out[place] = s.key_in ? s.order_in[i0 + j] : static_cast<int32_t>(i0 + j);
+        }
+        __syncwarp();
+    }
+}
+
+unsigned grid_for(int64_t words)
+{
+    const int64_t blocks = (words + kBlockWords - 1) / kBlockWords, most = static_cast<int64_t>(sm_count()) * 32;
+    return static_cast<unsigned>(blocks < most ? blocks : most);
 }
 
 cq_status check_table(int64_t T, int64_t V, int64_t K, int dtype, int ids64, const void *ids, const void *codes,
@@ -174,14 +450,54 @@ cq_status check_table(int64_t T, int64_t V, int64_t K, int dtype, int ids64, con
     return CQ_OK;
 }
 
-size_t round256(size_t n)
-{
-    return (n + 255) / 256 * 256;
-}
+// Where the gradient's workspace holds what.
+struct Workspace {
+    size_t key, order, key2, order2, counts, dots, head, tail, bytes;
+    Workspace(int64_t T, int64_t K)
+    {
+        const size_t n = static_cast<size_t>(T), ng = static_cast<size_t>(K / kGroup), chunks = (n + kChunk - 1) / kChunk;
+        const size_t sorted = T > kRankMost ? n * 4 : 0;
+        size_t at = 0;
+        auto take = [&](size_t size) {
+            const size_t here = at;
+            at += (size + 255) / 256 * 256;
+            return here;
+        };
+        key = take(n * 4);
+        order = take(n * 4);
+        key2 = take(sorted);
+        order2 = take(sorted);
+        counts = take(T > kRankMost ? (n + kSortTokens - 1) / kSortTokens * 256 * 4 : 0);
+        dots = take(n * ng * 4);
+        head = take(chunks * ng * 8);
+        tail = take(chunks * ng * 8);
+        bytes = at;
+    }
+};
 
-cq_status launched()
+cq_status sort_tokens(const Ids &ids, int64_t T, char *base, const Workspace &ws, cudaStream_t stream)
 {
-    return cudaGetLastError() == cudaSuccess ? CQ_OK : CQ_ERR_CUDA;
+    const unsigned blocks = static_cast<unsigned>((T + kSortTokens - 1) / kSortTokens);
+    int passes = 1;
+    while (passes < 4 && (ids.V >> (8 * passes)) != 0)
+        passes++;
+    uint32_t *keys[2] = {reinterpret_cast<uint32_t *>(base + ws.key), reinterpret_cast<uint32_t *>(base + ws.key2)};
+    int32_t *orders[2] = {reinterpret_cast<int32_t *>(base + ws.order), reinterpret_cast<int32_t *>(base + ws.order2)};
+    for (int i = 0; i < passes; i++) {
+        const int to = (passes - 1 - i) % 2;  // the last pass ends in the first pair
+        SortPass s = {i > 0 ? keys[1 - to] : nullptr, orders[1 - to], keys[to], orders[to],
+                      reinterpret_cast<int32_t *>(base + ws.counts), 8 * i};
+        sort_count_kernel<<<blocks, kThreads, 0, stream>>>(ids, T, s);
+        if (launched() != CQ_OK)
+            return CQ_ERR_CUDA;
+        sort_scan_kernel<<<1, 1024, 0, stream>>>(s.counts, static_cast<int64_t>(blocks) * 256);
+        if (launched() != CQ_OK)
+            return CQ_ERR_CUDA;
+        sort_scatter_kernel<<<blocks, kThreads, 0, stream>>>(ids, T, s);
+        if (launched() != CQ_OK)
+            return CQ_ERR_CUDA;
+    }
+    return CQ_OK;
 }
 
 }  // namespace
@@ -214,8 +530,7 @@ size_t cq_w4_embedding_backward_workspace_bytes(int64_t T, int64_t K)
 {
     if (T <= 0 || K <= 0)
         return 256;
-    const size_t n = static_cast<size_t>(T);
-    return round256(n * 8) + round256(n * 4) + round256(n * static_cast<size_t>(K / kGroup) * 4);
+    return Workspace(T, K).bytes;
 }
 
 cq_status cq_w4_embedding_backward(const void *dout, int dtype, const void *ids, int ids64, int64_t T, const uint32_t *codes,
@@ -229,31 +544,42 @@ cq_status cq_w4_embedding_backward(const void *dout, int dtype, const void *ids,
         return CQ_OK;
     if (!dscales || !is_aligned(dscales, 4) || (T > 0 && (!dout || !is_aligned(dout, 16))))
         return CQ_ERR_INVALID_ARG;
-    if (T > 0 && (!workspace || !is_aligned(workspace, 256) ||
-                  workspace_bytes < cq_w4_embedding_backward_workspace_bytes(T, K)))
-        return CQ_ERR_WORKSPACE;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int64_t ng = K / kGroup;
-    if (cudaMemsetAsync(dscales, 0, static_cast<size_t>(V) * ng * 4, s) != cudaSuccess)
-        return CQ_ERR_CUDA;
     if (T == 0)
-        return CQ_OK;
-    char *p = static_cast<char *>(workspace);
-    int64_t *key = reinterpret_cast<int64_t *>(p);
-    int32_t *order = reinterpret_cast<int32_t *>(p + round256(static_cast<size_t>(T) * 8));
-    float *dots = reinterpret_cast<float *>(p + round256(static_cast<size_t>(T) * 8) + round256(static_cast<size_t>(T) * 4));
+        return cudaMemsetAsync(dscales, 0, static_cast<size_t>(V) * ng * 4, s) == cudaSuccess ? CQ_OK : CQ_ERR_CUDA;
+    const Workspace ws(T, K);
+    if (!workspace || !is_aligned(workspace, 256) || workspace_bytes < ws.bytes)
+        return CQ_ERR_WORKSPACE;
+    char *base = static_cast<char *>(workspace);
+    uint32_t *key = reinterpret_cast<uint32_t *>(base + ws.key);
+    int32_t *order = reinterpret_cast<int32_t *>(base + ws.order);
+    float *dots = reinterpret_cast<float *>(base + ws.dots);
+    const Parts parts = {reinterpret_cast<double *>(base + ws.head), reinterpret_cast<double *>(base + ws.tail)};
     const Ids in = {ids, ids64, V};
-    auto kernel = dtype == CQ_DTYPE_BF16   ? token_dots_kernel<CQ_DTYPE_BF16>
-                  : dtype == CQ_DTYPE_FP16 ? token_dots_kernel<CQ_DTYPE_FP16>
-                                           : token_dots_kernel<CQ_DTYPE_FP32>;
-    kernel<<<grid_for(T * (K / 8)), kThreads, 0, s>>>(dout, in, T, codes, K / 8, dots);
+
+    constexpr int kRankBlock = kRankTokens * (kThreads / 32);
+    const int rank_blocks = T <= kRankMost ? static_cast<int>((T + kRankBlock - 1) / kRankBlock) : 0;
+    if (T > kRankMost && sort_tokens(in, T, base, ws, s) != CQ_OK)
+        return CQ_ERR_CUDA;
+    auto kernel = dtype == CQ_DTYPE_BF16   ? dots_kernel<CQ_DTYPE_BF16>
+                  : dtype == CQ_DTYPE_FP16 ? dots_kernel<CQ_DTYPE_FP16>
+                                           : dots_kernel<CQ_DTYPE_FP32>;
+    const int64_t words = T * (K / 8), zeros = V * ng / 4;  // a block's share of the zeros costs about as much as of the words
+    kernel<<<rank_blocks + grid_for(words > zeros ? words : zeros), kThreads, 0, s>>>(dout, in, T, codes, K / 8, dots, rank_blocks,
+                                                                                     key, order, dscales);
     if (launched() != CQ_OK)
         return CQ_ERR_CUDA;
-    rank_kernel<<<static_cast<unsigned>((T + kThreads - 1) / kThreads), kThreads, 0, s>>>(in, T, key, order);
+    int width = 1;
+    while (width < kThreads && width < ng)
+        width *= 2;
+    const int64_t chunks = (T + kChunk - 1) / kChunk, per_block = kThreads / width;
+    const unsigned grid = static_cast<unsigned>((chunks + per_block - 1) / per_block);
+    chunk_sums_kernel<<<grid, kThreads, 0, s>>>(key, order, T, V, dots, ng, width, multiplier, parts, dscales);
     if (launched() != CQ_OK)
         return CQ_ERR_CUDA;
-    run_sums_kernel<<<static_cast<unsigned>((T * ng + kThreads - 1) / kThreads), kThreads, 0, s>>>(key, order, T, V, dots, ng,
-                                                                                             multiplier, dscales);
+    if (chunks > 1)
+        join_runs_kernel<<<grid, kThreads, 0, s>>>(key, T, V, ng, width, multiplier, parts, dscales);
     return launched();
 }
 

@@ -137,24 +137,6 @@ struct Epilogue {
     int act;
 };
 
-template <class D>
-__device__ __forceinline__ void widen(const uint4 &u, float (&v)[8])
-{
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-        v[2 * j] = D::to_float(static_cast<uint16_t>(w[j]));
-        v[2 * j + 1] = D::to_float(static_cast<uint16_t>(w[j] >> 16));
-    }
-}
-
-template <class D>
-__device__ __forceinline__ uint4 narrow(const float (&v)[8])
-{
-    return make_uint4(D::from_floats(v[0], v[1]), D::from_floats(v[2], v[3]), D::from_floats(v[4], v[5]),
-                      D::from_floats(v[6], v[7]));
-}
-
 // A ring's slot and the parity of its phase.
 template <int kSlots>
 struct Ring {
@@ -909,22 +891,30 @@ __global__ void __cluster_dims__(kActCluster, 1, 1) __launch_bounds__(kActThread
     const int64_t col = col0 + 8 * lane;
     float acc[8] = {};
     if (col < R) {
-        for (int64_t t = rank * kActSlots + slot; t < T; t += kActCluster * kActSlots) {
-            const uint4 a = *reinterpret_cast<const uint4 *>(dy + t * lddy + col);
-            const uint4 b = *reinterpret_cast<const uint4 *>(pre + t * ldpre + col);
-            const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
-            uint32_t o[4];
+        constexpr int kAhead = 2;  // rows in flight per thread
+        constexpr int64_t kStep = kActCluster * kActSlots;
+        for (int64_t t = rank * kActSlots + slot; t < T; t += kAhead * kStep) {
+            uint4 a[kAhead], b[kAhead];
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                const float lo = D::to_float(static_cast<uint16_t>(av[j])) *
-                                 activation_slope(D::to_float(static_cast<uint16_t>(bv[j])), act);
-                const float hi = D::to_float(static_cast<uint16_t>(av[j] >> 16)) *
-                                 activation_slope(D::to_float(static_cast<uint16_t>(bv[j] >> 16)), act);
-                acc[2 * j] += lo;
-                acc[2 * j + 1] += hi;
-                o[j] = D::from_floats(lo, hi);
-            }
-            *reinterpret_cast<uint4 *>(dz + t * lddz + col) = make_uint4(o[0], o[1], o[2], o[3]);
+            for (int u = 0; u < kAhead; u++)
+                if (t + u * kStep < T) {
+                    a[u] = *reinterpret_cast<const uint4 *>(dy + (t + u * kStep) * lddy + col);
+                    b[u] = *reinterpret_cast<const uint4 *>(pre + (t + u * kStep) * ldpre + col);
+                }
+#pragma unroll
+            for (int u = 0; u < kAhead; u++)
+                if (t + u * kStep < T) {
+                    float d[8], z[8];
+                    widen<D>(a[u], d);
+                    widen<D>(b[u], z);
+                    slopes(z, act);
+#pragma unroll
+                    for (int j = 0; j < 8; j++) {
+                        z[j] *= d[j];
+                        acc[j] += z[j];
+                    }
+                    *reinterpret_cast<uint4 *>(dz + (t + u * kStep) * lddz + col) = narrow<D>(z);
+                }
         }
     }
 #pragma unroll
@@ -961,19 +951,6 @@ cq_status check_layer(int64_t T, int dtype, int64_t R, int64_t K, const void *qw
     return CQ_OK;
 }
 
-int sm_count()
-{
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 148;
-    return sms > 0 ? sms : 148;
-}
-
-cq_status launched()
-{
-    return cudaGetLastError() == cudaSuccess ? CQ_OK : CQ_ERR_CUDA;
-}
-
 template <class D>
 CUtensorMapDataType map_type()
 {
@@ -989,8 +966,8 @@ cq_status run_product(const uint16_t *act, int64_t ld, int64_t T, const Layer &w
         !tc::make_map(&word_map, CU_TENSOR_MAP_DATA_TYPE_INT32, 4, w.qweight, w.K / 8, w.R, w.R, kGradient ? kWordsPerGroup : kChunk / 8,
                       kGradient ? kChunk : kM, false))
         return CQ_ERR_CUDA;
-    auto kernel = weights_product_kernel<D, N, kGradient>;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Stages<N>::kBytes) != cudaSuccess)
+    constexpr auto kernel = weights_product_kernel<D, N, kGradient>;
+    if (allow_shared<kernel>(Stages<N>::kBytes) != cudaSuccess)
         return CQ_ERR_CUDA;
     const int64_t tiles = (rows + kM - 1) / kM * ((T + N - 1) / N), sms = sm_count();
     kernel<<<static_cast<unsigned>(tiles < sms ? tiles : sms), kTensorThreads, Stages<N>::kBytes, stream>>>(act_map, word_map, w, T, ep);
@@ -1036,8 +1013,8 @@ cq_status few_rows(const uint16_t *x, int64_t ldx, int64_t T, const Layer &w, co
     CUtensorMap word_map;
     if (!tc::make_map(&word_map, CU_TENSOR_MAP_DATA_TYPE_INT32, 4, w.qweight, w.K / 8, w.R, w.R, kWordsPerGroup, 32, true))
         return CQ_ERR_CUDA;
-    auto kernel = few_rows_kernel<D, NT>;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, FewStages<NT>::kBytes) != cudaSuccess)
+    constexpr auto kernel = few_rows_kernel<D, NT>;
+    if (allow_shared<kernel>(FewStages<NT>::kBytes) != cudaSuccess)
         return CQ_ERR_CUDA;
     cudaLaunchConfig_t config = {};
     config.gridDim = dim3(static_cast<unsigned>(tiles * ranks));
@@ -1073,8 +1050,8 @@ cq_status scale_gradient(const uint16_t *dz, int64_t lddz, const uint16_t *x, in
     if (!tc::make_map(&dz_map, map_type<D>(), 2, dz, T, w.R, lddz, kChunk, 64, true) ||
         !tc::make_map(&x_map, map_type<D>(), 2, x, T, w.K, ldx, kChunk, 64, true))
         return CQ_ERR_CUDA;
-    auto kernel = scale_gradient_kernel<D>;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGradBytes) != cudaSuccess)
+    constexpr auto kernel = scale_gradient_kernel<D>;
+    if (allow_shared<kernel>(kGradBytes) != cudaSuccess)
         return CQ_ERR_CUDA;
     const int64_t tiles = (w.R + kM - 1) / kM * ((w.K + kGradN - 1) / kGradN), sms = sm_count();
     kernel<<<static_cast<unsigned>(tiles < sms ? tiles : sms), kGradThreads, kGradBytes, stream>>>(dz_map, x_map, w, T, dscales);

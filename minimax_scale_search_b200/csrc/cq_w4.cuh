@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "cq.h"
@@ -110,30 +111,102 @@ __device__ __forceinline__ void activate(float (&z)[n], int act)
     }
 }
 
-__device__ __forceinline__ float activation_slope(float z, int act)
+// act'(z), to a few units of 2^-22 of its terms.
+template <int n>
+__device__ __forceinline__ void slopes(float (&z)[n], int act)
 {
-    constexpr float kC = 0.7978845608028654f;
-    switch (act) {
-    case CQ_ACT_RELU:
-        return z > 0.0f ? 1.0f : 0.0f;
-    case CQ_ACT_GELU:
-        return 0.5f * erfcf(z * -0.7071067811865476f) + z * (0.3989422804014327f * expf(-0.5f * z * z));
-    case CQ_ACT_GELU_TANH: {
-        const float t = tanhf(kC * (z + 0.044715f * z * z * z));
-        return 0.5f * (1.0f + t) + 0.5f * z * (1.0f - t * t) * (kC * (1.0f + 0.134145f * z * z));
-    }
-    case CQ_ACT_SILU: {
-        const float p = 1.0f / (1.0f + expf(-z));
-        return p * (1.0f + z * (1.0f - p));
-    }
-    default:
-        return 1.0f;
+    constexpr float kC = 0.7978845608028654f;  // sqrt(2 / pi)
+    if (act == CQ_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < n; i++)
+            z[i] = z[i] > 0.0f ? 1.0f : 0.0f;
+    } else if (act == CQ_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < n; i++)
+            z[i] = 0.5f * erfcf(z[i] * -0.7071067811865476f) + z[i] * (0.3989422804014327f * __expf(-0.5f * z[i] * z[i]));
+    } else if (act == CQ_ACT_GELU_TANH) {  // p = (1 + tanh u) / 2 = 1 / (1 + exp(-2u)), 1 - tanh^2 u = 4 p (1 - p)
+#pragma unroll
+        for (int i = 0; i < n; i++) {
+            const float q = z[i] * z[i], p = __fdividef(1.0f, 1.0f + __expf(-2.0f * kC * z[i] * (1.0f + 0.044715f * q)));
+            z[i] = p + z[i] * (2.0f * p * (1.0f - p)) * (kC * (1.0f + 0.134145f * q));
+        }
+    } else if (act == CQ_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < n; i++) {
+            const float p = __fdividef(1.0f, 1.0f + __expf(-z[i]));
+            z[i] = p * (1.0f + z[i] * (1.0f - p));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < n; i++)
+            z[i] = 1.0f;
     }
 }
 
 inline bool is_aligned(const void *p, size_t a)
 {
     return (reinterpret_cast<uintptr_t>(p) % a) == 0;
+}
+
+template <class D>
+__device__ __forceinline__ void widen(const uint4 &u, float (&v)[8])
+{
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        v[2 * j] = D::to_float(static_cast<uint16_t>(w[j]));
+        v[2 * j + 1] = D::to_float(static_cast<uint16_t>(w[j] >> 16));
+    }
+}
+
+template <class D>
+__device__ __forceinline__ uint4 narrow(const float (&v)[8])
+{
+    return make_uint4(D::from_floats(v[0], v[1]), D::from_floats(v[2], v[3]), D::from_floats(v[4], v[5]),
+                      D::from_floats(v[6], v[7]));
+}
+
+// SMs of the current device, and whether a kernel has been set up on it: asked once per device.
+constexpr int kMostDevices = 64;
+
+inline int current_device()
+{
+    int dev = -1;
+    return cudaGetDevice(&dev) == cudaSuccess ? dev : -1;
+}
+
+inline int sm_count()
+{
+    static std::atomic<int> known[kMostDevices];
+    const int dev = current_device();
+    if (dev >= 0 && dev < kMostDevices && known[dev].load(std::memory_order_relaxed) > 0)
+        return known[dev].load(std::memory_order_relaxed);
+    int sms = 0;
+    if (dev < 0 || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
+        return 148;
+    if (dev < kMostDevices)
+        known[dev].store(sms, std::memory_order_relaxed);
+    return sms;
+}
+
+// Lets `kernel` have `bytes` of dynamic shared memory on the current device.
+template <auto kernel>
+cudaError_t allow_shared(int bytes)
+{
+    static std::atomic<bool> done[kMostDevices];
+    const int dev = current_device();
+    const bool kept = dev >= 0 && dev < kMostDevices;
+    if (kept && done[dev].load(std::memory_order_relaxed))
+        return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && kept)
+        done[dev].store(true, std::memory_order_relaxed);
+    return e;
+}
+
+inline cq_status launched()
+{
+    return cudaGetLastError() == cudaSuccess ? CQ_OK : CQ_ERR_CUDA;
 }
 
 // A [T][n] operand of 16-bit values: 16-byte rows.
