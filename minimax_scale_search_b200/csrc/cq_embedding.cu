@@ -3,8 +3,8 @@
 // The table is the selection's own output for a [V][K] matrix: scales
 // [V * K/128] and code words [V * K/128][16], so a row's words are contiguous.
 //
-// Lookup.  out[t] = m s q of row ids[t]; the bytes of the output bound it.  A thread takes four
-// words (8 values each) 256 words apart, all their loads before the first store.
+// Lookup.  out[t] = m s q of row ids[t]; the bytes of the output bound it.  Sixteen lanes have a unit of up to
+// four groups of one token (a word of 8 values of each group a lane), all their loads before the first store.
 //
 // Gradient.  dscales[v][g] = m sum_{t: ids[t] = v} sum_{i in g} dout[t][i] q[v][i], in
 // three launches:
@@ -12,23 +12,24 @@
 //     bounds the whole); the same launch fills dscales with zeros and sorts the tokens by
 //     (id, t): up to kRankMost tokens by counting, for each, the tokens before it (T^2
 //     comparisons, no further launch), above with a radix sort of its own launches;
-//  2. sums over the runs of equal ids within each chunk of 64 sorted tokens, in fp64; a run that
+//  2. sums over the runs of equal ids within each chunk of 8 sorted tokens, in fp64; a run that
 //     lies inside a chunk is done, others leave a part at the chunk's head or tail;
 //  3. the runs across chunks, from their parts in order.
 // So a row that every token names is summed by many threads, and the order of the sums is fixed.
+#include <type_traits>
+
 #include "cq_w4.cuh"
 
 namespace cq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWordsAhead = 4;                          // words per thread in flight
-constexpr int kBlockWords = kThreads * kWordsAhead;
-constexpr int kRankMost = 16384;                        // tokens sorted by counting
-constexpr int kRankTokens = 8;                          // per warp
-constexpr int kRankTile = 1024;                         // keys in shared memory
-constexpr int kChunk = 64;                              // sorted tokens per partial sum
-constexpr int kSortTokens = 4096;                       // per CTA of the radix sort
+constexpr int kUnits = kThreads / kWordsPerGroup;       // units of a CTA at a time: kGroups groups of one token
+constexpr int kRankMost = 8192;                         // tokens sorted by counting
+constexpr int kRankBlock = 32;                          // tokens ranked by a CTA, one a lane
+constexpr int kRankTile = kRankMost;                    // keys in shared memory at a time: all (tiles of 1024 were slower, 28 us for 18)
+constexpr int kChunk = 8;                               // sorted tokens per partial sum
+constexpr int kSortTokens = 1024;                       // per CTA of the radix sort
 
 struct Ids {
     const void *p;
@@ -42,24 +43,44 @@ struct Ids {
     }
 };
 
-// i / d and i mod d, in 32 bits where they fit.
-__device__ __forceinline__ void divide(int64_t i, int64_t d, bool narrow, int64_t &q, int64_t &r)
-{
-    if (narrow) {
-        q = static_cast<uint32_t>(i) / static_cast<uint32_t>(d);
-        r = static_cast<uint32_t>(i) - static_cast<uint32_t>(q) * static_cast<uint32_t>(d);
-    } else {
-        q = i / d;
-        r = i - q * d;
+// Division by the units of a row.  Below 2^31: i d^-1 as a product with ceil(2^(31+s) / d), 2^(s-1) < d <= 2^s,
+// whose excess of less than 2^-31 i / 2^s < 1 / d never reaches the next quotient.
+struct Divider {
+    int64_t d;
+    uint32_t factor;  // 0: 64-bit division, or by one
+    int shift;
+    Divider(int64_t d, int64_t n) : d(d), factor(0), shift(0)
+    {
+        if (d == 1 || n >= (static_cast<int64_t>(1) << 31))
+            return;
+        while ((static_cast<int64_t>(1) << shift) < d)
+            shift++;
+        factor = static_cast<uint32_t>(((static_cast<uint64_t>(1) << (31 + shift)) + d - 1) / d);
+        shift--;  // the product's upper half is taken first
     }
-}
+    __device__ __forceinline__ void operator()(int64_t i, int64_t &q, int64_t &r) const
+    {
+        if (factor) {
+            const uint32_t n = static_cast<uint32_t>(i), k = __umulhi(n, factor) >> shift;
+            q = k;
+            r = n - k * static_cast<uint32_t>(d);
+        } else {
+            q = d == 1 ? i : i / d;
+            r = i - q * d;
+        }
+    }
+};
 
-// Eight values from a code word: q = u - 8.
-__device__ __forceinline__ void unpack(uint32_t word, float (&q)[8])
+// Eight values u - 8 from a code word: pairs in binary16, where 1024 | u is 1024 + u.
+__device__ __forceinline__ void unpack(uint32_t word, uint32_t low, float (&q)[8])
 {
 #pragma unroll
-    for (int j = 0; j < 8; j++)
-        q[j] = static_cast<float>(static_cast<int>((word >> (4 * j)) & 15u) - 8);
+    for (int j = 0; j < 4; j++) {
+        const uint32_t n = FP16::sub(((word >> (4 * j)) & low) | FP16::kMagic, FP16::kMagic + 0x00080008u);
+        const float2 f = __half22float2(reinterpret_cast<const __half2 &>(n));
+        q[j] = f.x;
+        q[j + 4] = f.y;
+    }
 }
 
 template <int DT>
@@ -99,147 +120,167 @@ struct Eight {
     }
 };
 
-template <int DT>
+template <int DT, int kGroups>
 __global__ void __launch_bounds__(kThreads) embedding_kernel(Ids ids, int64_t T, const uint16_t *__restrict__ scales,
-                                                             const uint32_t *__restrict__ codes, int64_t K8, float multiplier,
-                                                             void *__restrict__ out)
+                                                             const uint32_t *__restrict__ codes, int64_t ng, Divider by,
+                                                             uint32_t low, float multiplier, void *__restrict__ out)
 {
-    const int64_t n = T * K8;
-    const bool narrow = n < (static_cast<int64_t>(1) << 32);
-    for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kBlockWords + threadIdx.x; i0 < n;
-         i0 += static_cast<int64_t>(gridDim.x) * kBlockWords) {
-        uint32_t word[kWordsAhead], row[kWordsAhead];
-        uint16_t scale[kWordsAhead];
-        int64_t k[kWordsAhead];
+    const int lane = threadIdx.x % kWordsPerGroup;
+    for (int64_t unit = static_cast<int64_t>(blockIdx.x) * kUnits + threadIdx.x / kWordsPerGroup; unit < T * by.d;
+         unit += static_cast<int64_t>(gridDim.x) * kUnits) {
+        int64_t t, b;
+        by(unit, t, b);
+        const uint32_t row = ids.key(t);
+        const bool named = row < ids.V;
+        const int64_t g0 = b * kGroups;
+        const int n = ng - g0 < kGroups ? static_cast<int>(ng - g0) : kGroups;
+        const int64_t from = row * ng + g0;
+        uint32_t word[kGroups];
+        uint16_t scale[kGroups];
 #pragma unroll
-        for (int u = 0; u < kWordsAhead; u++) {
-            const int64_t i = i0 + u * kThreads;
-            int64_t t = 0;
-            if (i < n)
-                divide(i, K8, narrow, t, k[u]);
-            row[u] = i < n ? ids.key(t) : static_cast<uint32_t>(ids.V);
-        }
-#pragma unroll
-        for (int u = 0; u < kWordsAhead; u++)
-            if (row[u] < ids.V) {
-                word[u] = codes[row[u] * K8 + k[u]];
-                scale[u] = scales[row[u] * (K8 / kWordsPerGroup) + k[u] / kWordsPerGroup];
+        for (int u = 0; u < kGroups; u++)
+            if (named && u < n) {
+                word[u] = codes[(from + u) * kWordsPerGroup + lane];
+                scale[u] = scales[from + u];
             }
 #pragma unroll
-        for (int u = 0; u < kWordsAhead; u++) {
-            const int64_t i = i0 + u * kThreads;
-            if (i >= n)
+        for (int u = 0; u < kGroups; u++) {
+            if (u >= n)
                 break;
             float q[8] = {};
-            if (row[u] < ids.V) {
+            if (named) {
                 const float s = half_bits(scale[u]);
-                unpack(word[u], q);
+                unpack(word[u], low, q);
 #pragma unroll
                 for (int j = 0; j < 8; j++)
                     q[j] = multiplier * (s * q[j]);
             }
-            store8<DT>(out, i * 8, q);
+            store8<DT>(out, ((t * ng + g0 + u) * kWordsPerGroup + lane) * 8, q);
         }
     }
 }
 
 // ---- gradient ------------------------------------------------------------------------------------
 
-// order[rank] = t, key[rank] = row: a warp counts, for eight tokens, the tokens before
-// each by (row, t).
-__device__ void rank_tokens(const Ids &ids, int T, int warps_before, uint32_t *key, int32_t *order)
+// order[rank] = t, key[rank] = row: for each of a CTA's 32 tokens, one a lane, the number of tokens before it
+// by (row, t).  The warps take an eighth of the tokens each to compare with, four per shared read.
+// (128 tokens per CTA, four a lane, had fewer reads and took twice as long: too few CTAs.)
+__device__ void rank_tokens(const Ids &ids, int T, int t0, uint32_t *key, int32_t *order)
 {
-    __shared__ uint32_t tile[kRankTile];
-    const int lane = threadIdx.x % 32;
-    const int t0 = (warps_before + static_cast<int>(threadIdx.x) / 32) * kRankTokens;
-    uint32_t mine[kRankTokens];
-    int rank[kRankTokens] = {};
+    constexpr int kWarps = kThreads / 32;
+    __shared__ alignas(16) uint32_t tile[kRankTile];
+    __shared__ int ranks[kWarps][kRankBlock];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, t = t0 + lane;
+    const uint32_t mine = t < T ? ids.key(t) : 0;
+    int rank = 0;
+    static_assert(kRankTile % kThreads == 0 && kThreads % (32 * kWarps) == 0 && kRankBlock == 32, "shares are blocks of 32");
+    const int end = (T + kThreads - 1) / kThreads * kThreads;  // the keys that are there, and some that are above all
+#pragma unroll 8
+    for (int j = threadIdx.x; j < end; j += kThreads)
+        tile[j] = j < T ? ids.key(j) : 0xFFFFFFFFu;
+    __syncthreads();
+    // (other, j) < (mine, t)  <=>  other < mine + (j < t)
+    const int share = end / kWarps;  // % 32 == 0
+    for (int j0 = warp * share; j0 < (warp + 1) * share; j0 += 32) {
+        if (j0 != t0) {
+            const uint32_t below = mine + (j0 < t0);
+            const uint4 *p = reinterpret_cast<const uint4 *>(tile + j0);
 #pragma unroll
-    for (int i = 0; i < kRankTokens; i++)
-        mine[i] = t0 + i < T ? ids.key(t0 + i) : 0;
-    for (int j0 = 0; j0 < T; j0 += kRankTile) {
-        __syncthreads();
-        for (int j = threadIdx.x; j < kRankTile; j += kThreads)
-            tile[j] = j0 + j < T ? ids.key(j0 + j) : 0xFFFFFFFFu;
-        __syncthreads();
-        for (int j = lane; j < kRankTile; j += 32) {
-            const uint32_t other = tile[j];
-            const int at = j0 + j;
-            // (other, at) < (mine, t)  <=>  other < mine + (at < t); the eight t are adjacent
-            if (at - lane + 31 < t0) {
-#pragma unroll
-                for (int i = 0; i < kRankTokens; i++)
-                    rank[i] += other <= mine[i];
-            } else {
-#pragma unroll
-                for (int i = 0; i < kRankTokens; i++)
-                    rank[i] += other < mine[i] + (at < t0 + i);
-            }
+            for (int j = 0; j < 8; j++)
+                rank += (p[j].x < below) + (p[j].y < below) + (p[j].z < below) + (p[j].w < below);
+        } else {
+            for (int j = j0; j < j0 + 32; j++)
+                rank += tile[j] < mine + (j < t);
         }
     }
+    ranks[warp][lane] = rank;
+    __syncthreads();
+    if (warp == 0 && t < T) {
+        int r = 0;
 #pragma unroll
-    for (int i = 0; i < kRankTokens; i++) {
-        const int r = __reduce_add_sync(0xFFFFFFFFu, rank[i]);
-        if (lane == i && t0 + i < T) {
-            key[r] = mine[i];
-            order[r] = t0 + i;
-        }
+        for (int i = 0; i < kWarps; i++)
+            r += ranks[i][lane];
+        key[r] = mine;
+        order[r] = t;
     }
 }
 
-// Blocks below `rank_blocks` sort by counting; the others form the dots (16 lanes per group) and
-// write the zeros.
-template <int DT>
+// Sums of kGroups values over 16 lanes, in a fixed order: the sum of value u in lane u * 16 / kGroups.
+template <int kGroups>
+__device__ __forceinline__ float sum_lanes(float (&v)[kGroups], int lane)
+{
+    int n = kGroups;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
+        if (n > 1) {  // a lane keeps half of its values and gets its partner's parts of them
+            n /= 2;
+#pragma unroll
+            for (int u = 0; u < kGroups / 2; u++)
+                if (u < n) {
+                    const bool upper = lane & o;
+                    const float give = upper ? v[u] : v[u + n];
+                    v[u] = (upper ? v[u + n] : v[u]) + __shfl_xor_sync(0xFFFFFFFFu, give, o, 16);
+                }
+        } else {
+            v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], o, 16);
+        }
+    }
+    return v[0];
+}
+
+// Blocks below `rank_blocks` sort by counting; the others form the dots and write the zeros.
+template <int DT, int kGroups>
 __global__ void __launch_bounds__(kThreads) dots_kernel(const void *__restrict__ dout, Ids ids, int64_t T,
-                                                        const uint32_t *__restrict__ codes, int64_t K8, float *__restrict__ dots,
-                                                        int rank_blocks, uint32_t *key, int32_t *order, float *__restrict__ dscales)
+                                                        const uint32_t *__restrict__ codes, int64_t ng, Divider by, uint32_t low,
+                                                        float *__restrict__ dots, int rank_blocks, uint32_t *key, int32_t *order,
+                                                        float *__restrict__ dscales)
 {
     if (static_cast<int>(blockIdx.x) < rank_blocks) {
-        rank_tokens(ids, static_cast<int>(T), blockIdx.x * (kThreads / 32), key, order);
+        rank_tokens(ids, static_cast<int>(T), blockIdx.x * kRankBlock, key, order);
         return;
     }
     const int64_t block = blockIdx.x - rank_blocks, blocks = gridDim.x - rank_blocks;
-    const int64_t n = T * K8;
-    const bool narrow = n < (static_cast<int64_t>(1) << 32);
-    for (int64_t b0 = block * kBlockWords; b0 < n; b0 += blocks * kBlockWords) {
-        uint32_t word[kWordsAhead];
-        Eight<DT> d[kWordsAhead];
-        bool named[kWordsAhead];
+    const int lane = threadIdx.x % kWordsPerGroup;
+    for (int64_t unit0 = block * kUnits; unit0 < T * by.d; unit0 += blocks * kUnits) {
+        const int64_t unit = unit0 + threadIdx.x / kWordsPerGroup;
+        float v[kGroups] = {};
+        int64_t t = 0, g0 = 0;
+        int n = 0;
+        if (unit < T * by.d) {
+            int64_t b;
+            by(unit, t, b);
+            g0 = b * kGroups;
+            n = ng - g0 < kGroups ? static_cast<int>(ng - g0) : kGroups;
+            uint32_t word[kGroups];
+            Eight<DT> d[kGroups];
 #pragma unroll
-        for (int u = 0; u < kWordsAhead; u++) {
-            const int64_t i = b0 + u * kThreads + threadIdx.x;  // n % 16 == 0: a half-warp in or out together
-            named[u] = false;
-            if (i < n) {
-                int64_t t, k;
-                divide(i, K8, narrow, t, k);
-                const uint32_t v = ids.key(t);
-                named[u] = v < ids.V;
-                if (named[u]) {
-                    d[u].load(dout, i * 8);
-                    word[u] = codes[v * K8 + k];
-                }
+            for (int u = 0; u < kGroups; u++)
+                if (u < n)
+                    d[u].load(dout, ((t * ng + g0 + u) * kWordsPerGroup + lane) * 8);  // does not wait for the id
+            const uint32_t row = ids.key(t);
+            if (row < ids.V) {
+#pragma unroll
+                for (int u = 0; u < kGroups; u++)
+                    if (u < n)
+                        word[u] = codes[(row * ng + g0 + u) * kWordsPerGroup + lane];
+#pragma unroll
+                for (int u = 0; u < kGroups; u++)
+                    if (u < n) {
+                        float x[8], q[8];
+                        d[u].values(x);
+                        unpack(word[u], low, q);
+#pragma unroll
+                        for (int j = 0; j < 8; j++)
+                            v[u] = fmaf(x[j], q[j], v[u]);
+                    }
             }
         }
-#pragma unroll
-        for (int u = 0; u < kWordsAhead; u++) {
-            const int64_t i = b0 + u * kThreads + threadIdx.x;
-            float s = 0.0f;
-            if (named[u]) {
-                float x[8], q[8];
-                d[u].values(x);
-                unpack(word[u], q);
-#pragma unroll
-                for (int j = 0; j < 8; j++)
-                    s = fmaf(x[j], q[j], s);
-            }
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1)
-                s += __shfl_xor_sync(0xFFFFFFFFu, s, o, 16);
-            if (i < n && (threadIdx.x & 15) == 0)
-                dots[i / kWordsPerGroup] = s;
-        }
+        const float sum = sum_lanes<kGroups>(v, lane);
+        constexpr int kSpread = kWordsPerGroup / kGroups;
+        if (lane % kSpread == 0 && lane / kSpread < n)
+            dots[t * ng + g0 + lane / kSpread] = sum;
     }
-    const int64_t outputs = ids.V * (K8 / kWordsPerGroup);
+    const int64_t outputs = ids.V * ng;
     for (int64_t i = block * kThreads + threadIdx.x; i < outputs; i += blocks * kThreads)
         dscales[i] = 0.0f;
 }
@@ -273,7 +314,7 @@ __global__ void __launch_bounds__(kThreads) chunk_sums_kernel(const uint32_t *__
             else
                 dscales[current * ng + g] = static_cast<float>(sum * multiplier);
         };
-        constexpr int kAhead = 8;
+        constexpr int kAhead = kChunk;
         for (int64_t p = p0; p < p1; p += kAhead) {
             uint32_t k[kAhead];
             float d[kAhead];
@@ -299,30 +340,49 @@ __global__ void __launch_bounds__(kThreads) chunk_sums_kernel(const uint32_t *__
     }
 }
 
-// Runs that begin in chunk c and go on after it.
+// Runs that begin in chunk c and go on after it, a warp for each: `width` lanes (a power of two) have
+// a group each, 32 / width of them share its parts.
 __global__ void __launch_bounds__(kThreads) join_runs_kernel(const uint32_t *__restrict__ key, int64_t T, int64_t V, int64_t ng,
                                                              int width, float multiplier, Parts parts, float *__restrict__ dscales)
 {
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * (kThreads / width) + threadIdx.x / width, p0 = c * kChunk;
+    const int lane = threadIdx.x % 32;
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32, p0 = c * kChunk;
     if (p0 + kChunk >= T)
         return;
     const uint32_t v = key[p0 + kChunk];
     if (v >= V || key[p0 + kChunk - 1] != v || (p0 > 0 && key[p0 - 1] == v))
         return;
-    int64_t last = c + 1, beyond = (T - 1) / kChunk + 1;  // the last chunk that begins with v
-    while (beyond - last > 1) {
-        const int64_t mid = (last + beyond) / 2;
-        if (key[mid * kChunk] == v)
-            last = mid;
-        else
-            beyond = mid;
+    // the last chunk that begins with v: 32 candidates at once, 32 chunks apart, then the 31 after the last hit
+    const int64_t chunks = (T - 1) / kChunk + 1;
+    auto begins = [&](int64_t i) { return i < chunks && key[i * kChunk] == v; };
+    int64_t last = c + 1;
+    for (int hits = 32; hits == 32;) {
+        hits = __popc(__ballot_sync(0xFFFFFFFFu, begins(last + 32 * (lane + 1))));
+        last += 32 * hits;
     }
-    for (int64_t g = threadIdx.x % width; g < ng; g += width) {
-        double sum = parts.tail[c * ng + g];
-#pragma unroll 8
-        for (int64_t i = c + 1; i <= last; i++)
-            sum += parts.head[i * ng + g];
-        dscales[v * ng + g] = static_cast<float>(sum * multiplier);
+    last += __popc(__ballot_sync(0xFFFFFFFFu, begins(last + lane + 1)));
+    const int shares = 32 / width, share = lane / width;
+    for (int64_t g0 = 0; g0 < ng; g0 += width) {
+        const int64_t g = g0 + lane % width;
+        double sum = 0.0;
+        if (g < ng) {
+            constexpr int kAhead = 16;
+            for (int64_t i = c + 1 + share; i <= last; i += kAhead * shares) {
+                double part[kAhead];
+#pragma unroll
+                for (int u = 0; u < kAhead; u++)
+                    part[u] = i + u * shares <= last ? parts.head[(i + u * shares) * ng + g] : 0.0;
+#pragma unroll
+                for (int u = 0; u < kAhead; u++)
+                    sum += part[u];
+            }
+            if (share == 0)
+                sum += parts.tail[c * ng + g];
+        }
+        for (int o = 16; o >= width; o >>= 1)
+            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        if (g < ng && share == 0)
+            dscales[v * ng + g] = static_cast<float>(sum * multiplier);
     }
 }
 
@@ -359,10 +419,16 @@ __global__ void __launch_bounds__(1024) sort_scan_kernel(int32_t *counts, int64_
 {
     __shared__ int32_t sums[32];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    constexpr int kEach = 8;  // counts per thread, n % 256 == 0
     int32_t before = 0;
-    for (int64_t i0 = 0; i0 < n; i0 += 1024) {
-        const int64_t i = i0 + threadIdx.x;
-        const int32_t mine = i < n ? counts[i] : 0;
+    for (int64_t i0 = 0; i0 < n; i0 += 1024 * kEach) {
+        const int64_t i = i0 + threadIdx.x * kEach;
+        int4 a = make_int4(0, 0, 0, 0), b = a;
+        if (i < n) {
+            a = *reinterpret_cast<const int4 *>(counts + i);
+            b = *reinterpret_cast<const int4 *>(counts + i + 4);
+        }
+        const int32_t mine = a.x + a.y + a.z + a.w + b.x + b.y + b.z + b.w;
         int32_t x = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -378,16 +444,28 @@ __global__ void __launch_bounds__(1024) sort_scan_kernel(int32_t *counts, int64_
             const int32_t y = __shfl_up_sync(0xFFFFFFFFu, w, o);
             w += lane >= o ? y : 0;
         }
-        const int32_t warps_before = warp > 0 ? __shfl_sync(0xFFFFFFFFu, w, (warp + 31) % 32) : 0;
+        const int32_t warps_before = __shfl_sync(0xFFFFFFFFu, w, (warp + 31) % 32);
         const int32_t total = __shfl_sync(0xFFFFFFFFu, w, 31);
-        if (i < n)
-            counts[i] = before + warps_before + x - mine;
+        if (i < n) {
+            int32_t at = before + (warp > 0 ? warps_before : 0) + x - mine;
+            int4 p, q;
+            p.x = at;
+            p.y = at += a.x;
+            p.z = at += a.y;
+            p.w = at += a.z;
+            q.x = at += a.w;
+            q.y = at += b.x;
+            q.z = at += b.y;
+            q.w = at += b.z;
+            *reinterpret_cast<int4 *>(counts + i) = p;
+            *reinterpret_cast<int4 *>(counts + i + 4) = q;
+        }
         before += total;
         __syncthreads();
     }
 }
 
-// A warp has 512 tokens in a row; first its digits' counts, then each token's place: the digit's
+// A warp has 128 tokens in a row; first its digits' counts, then each token's place: the digit's
 // start, the warps before, the warp's tokens before.
 __global__ void __launch_bounds__(kThreads) sort_scatter_kernel(Ids ids, int64_t T, SortPass s)
 {
@@ -430,10 +508,19 @@ __global__ void __launch_bounds__(kThreads) sort_scatter_kernel(Ids ids, int64_t
     }
 }
 
-unsigned grid_for(int64_t words)
+// CTAs for so many units.
+unsigned grid_for(int64_t units)
 {
-    const int64_t blocks = (words + kBlockWords - 1) / kBlockWords, most = static_cast<int64_t>(sm_count()) * 32;
+    const int64_t blocks = (units + kUnits - 1) / kUnits, most = static_cast<int64_t>(sm_count()) * 32;
     return static_cast<unsigned>(blocks < most ? blocks : most);
+}
+
+// Four groups to a unit where rows have them; a single one for rows of one to three groups, whose
+// units would stand idle in part.
+template <class F>
+cq_status by_groups(int64_t ng, F run)
+{
+    return ng >= 4 ? run(std::integral_constant<int, 4>()) : run(std::integral_constant<int, 1>());
 }
 
 cq_status check_table(int64_t T, int64_t V, int64_t K, int dtype, int ids64, const void *ids, const void *codes,
@@ -518,12 +605,18 @@ cq_status cq_w4_embedding(const void *ids, int ids64, int64_t T, const uint16_t 
     if ((V > 0 && (!scales || !is_aligned(scales, 2))) || !out || !is_aligned(out, 16))
         return CQ_ERR_INVALID_ARG;
     const Ids in = {ids, ids64, V};
-    auto kernel = dtype == CQ_DTYPE_BF16   ? embedding_kernel<CQ_DTYPE_BF16>
-                  : dtype == CQ_DTYPE_FP16 ? embedding_kernel<CQ_DTYPE_FP16>
-                                           : embedding_kernel<CQ_DTYPE_FP32>;
-    kernel<<<grid_for(T * (K / 8)), kThreads, 0, static_cast<cudaStream_t>(stream)>>>(in, T, scales, codes, K / 8,
-                                                                                      multiplier, out);
-    return launched();
+    const int64_t ng = K / kGroup;
+    auto run = [&](auto groups) {
+        constexpr int kGroups = decltype(groups)::value;
+        const int64_t units = (ng + kGroups - 1) / kGroups;
+        auto kernel = dtype == CQ_DTYPE_BF16   ? embedding_kernel<CQ_DTYPE_BF16, kGroups>
+                      : dtype == CQ_DTYPE_FP16 ? embedding_kernel<CQ_DTYPE_FP16, kGroups>
+                                               : embedding_kernel<CQ_DTYPE_FP32, kGroups>;
+        kernel<<<grid_for(T * units), kThreads, 0, static_cast<cudaStream_t>(stream)>>>(in, T, scales, codes, ng,
+                                                                                        Divider(units, T * units), kLow, multiplier, out);
+        return launched();
+    };
+    return by_groups(ng, run);
 }
 
 size_t cq_w4_embedding_backward_workspace_bytes(int64_t T, int64_t K)
@@ -558,18 +651,21 @@ cq_status cq_w4_embedding_backward(const void *dout, int dtype, const void *ids,
     const Parts parts = {reinterpret_cast<double *>(base + ws.head), reinterpret_cast<double *>(base + ws.tail)};
     const Ids in = {ids, ids64, V};
 
-    constexpr int kRankBlock = kRankTokens * (kThreads / 32);
     const int rank_blocks = T <= kRankMost ? static_cast<int>((T + kRankBlock - 1) / kRankBlock) : 0;
     if (T > kRankMost && sort_tokens(in, T, base, ws, s) != CQ_OK)
         return CQ_ERR_CUDA;
-    auto kernel = dtype == CQ_DTYPE_BF16   ? dots_kernel<CQ_DTYPE_BF16>
-                  : dtype == CQ_DTYPE_FP16 ? dots_kernel<CQ_DTYPE_FP16>
-                                           : dots_kernel<CQ_DTYPE_FP32>;
-    const int64_t words = T * (K / 8), zeros = V * ng / 4;  // a block's share of the zeros costs about as much as of the words
-    kernel<<<rank_blocks + grid_for(words > zeros ? words : zeros), kThreads, 0, s>>>(dout, in, T, codes, K / 8, dots, rank_blocks,
-                                                                                     key, order, dscales);
-    if (launched() != CQ_OK)
-        return CQ_ERR_CUDA;
+    const cq_status made = by_groups(ng, [&](auto groups) {
+        constexpr int kGroups = decltype(groups)::value;
+        auto kernel = dtype == CQ_DTYPE_BF16   ? dots_kernel<CQ_DTYPE_BF16, kGroups>
+                      : dtype == CQ_DTYPE_FP16 ? dots_kernel<CQ_DTYPE_FP16, kGroups>
+                                               : dots_kernel<CQ_DTYPE_FP32, kGroups>;
+        const int64_t units = (ng + kGroups - 1) / kGroups, zeros = V * ng / 256;  // a CTA's share of zeros costs about one unit
+        kernel<<<rank_blocks + grid_for(T * units > zeros ? T * units : zeros), kThreads, 0, s>>>(
+            dout, in, T, codes, ng, Divider(units, T * units), kLow, dots, rank_blocks, key, order, dscales);
+        return launched();
+    });
+    if (made != CQ_OK)
+        return made;
     int width = 1;
     while (width < kThreads && width < ng)
         width *= 2;
@@ -579,7 +675,8 @@ cq_status cq_w4_embedding_backward(const void *dout, int dtype, const void *ids,
     if (launched() != CQ_OK)
         return CQ_ERR_CUDA;
     if (chunks > 1)
-        join_runs_kernel<<<grid, kThreads, 0, s>>>(key, T, V, ng, width, multiplier, parts, dscales);
+        join_runs_kernel<<<static_cast<unsigned>((chunks + kThreads / 32 - 1) / (kThreads / 32)), kThreads, 0, s>>>(
+            key, T, V, ng, width < 32 ? width : 32, multiplier, parts, dscales);
     return launched();
 }
 

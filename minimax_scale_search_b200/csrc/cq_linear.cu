@@ -286,14 +286,6 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
 #pragma unroll
             for (int j = 0; j < kSetWords; j++)
                 word[j] = words[j * kOutputs];
-            __syncwarp();
-            if (lane == 0)
-                tc::barrier_arrive(raw_empty(raw));
-            raw += kUnpackSets;
-            if (raw >= S::kRaw) {
-                raw -= S::kRaw;
-                raw_parity ^= 1;
-            }
             uint4 values[kSetWords];
 #pragma unroll
             for (int j = 0; j < kSetWords; j++)
@@ -306,8 +298,17 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
                 *reinterpret_cast<uint4 *>(to + (((k8 + j) & 7) ^ (r & 7)) * 16) = values[j];
             tc::fence_shared_writes();
             __syncwarp();
-            if (lane == 0)
+            // The words are released only here, after stores that needed them: an arrival does not wait for
+            // shared loads in flight, and with shared memory busy the next words overtook them.
+            if (lane == 0) {
+                tc::barrier_arrive(raw_empty(raw));
                 tc::barrier_arrive(full(op.slot));
+            }
+            raw += kUnpackSets;
+            if (raw >= S::kRaw) {
+                raw -= S::kRaw;
+                raw_parity ^= 1;
+            }
             op.skip(kUnpackSets);
         }
     } else if (warp == kCopyWarp) {  // activations, by tensor map
@@ -640,8 +641,11 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                             total[2 * m + p][n][k] = fmaf(s[2 * p + (k >> 1)], acc[2 * m + p][n][k], total[2 * m + p][n][k]);
             }
             __syncwarp();
+            // The arrival's address hangs on sums that hang on every shared load above (w.low is kLow): on its own
+            // it would not wait for loads in flight.
+            const uint32_t loaded = (__float_as_uint(total[0][0][0]) ^ __float_as_uint(total[2][NT - 1][0])) & (w.low ^ kLow);
             if (lane == 0)
-                tc::barrier_arrive(empty(slot));
+                tc::barrier_arrive(empty(slot) + loaded);
             slot += kFewSets;
             if (slot >= S::kStages) {
                 slot -= S::kStages;
@@ -868,68 +872,59 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         tc::tmem_free(tmem, 2 * kGradN);
 }
 
-constexpr int kActCluster = 8;
-constexpr int kActSlab = 64;                          // columns per cluster
-constexpr int kActSlots = 32;                         // row slots per CTA: 8 lanes x 8 columns cover a slab's row
-constexpr int kActThreads = kActSlots * kActSlab / 8;
-
-// dz = dy act'(pre) and its column sums.  A cluster of 8 CTAs owns 64 columns; its 256
-// row slots take every 256th row, a thread 8 adjacent columns (16-byte accesses).  The
-// sums meet in shared memory and through distributed shared memory, in a fixed order.
+// dz = dy act'(pre) and its column sums.  A cluster of 8 CTAs owns 64 columns; its
+// 256 row slots take every 256th row, a thread 8 adjacent columns (16-byte accesses; two rows at a time were slower,
+// 86 us for 76).  The sums meet in shared memory and through distributed shared memory, in a fixed order.
 // Bound by HBM: 6 bytes per element.
+constexpr int kActCluster = 8;
+constexpr int kActThreads = 256;
+constexpr int kActColumns = 64;    // pieces of 128 bytes of a row (76 us for 4,096 x 14,336 silu; 256 bytes 79 us)
+
 template <class D>
 __global__ void __cluster_dims__(kActCluster, 1, 1) __launch_bounds__(kActThreads)
     activation_backward_kernel(const uint16_t *dy, int64_t lddy, const uint16_t *pre, int64_t ldpre, int64_t T, int64_t R,
                                int act, uint16_t *dz, int64_t lddz, float *dbias)
 {
-    __shared__ float part[kActSlots][kActSlab];
-    __shared__ float cta_sum[kActSlab];
+    constexpr int kLanes = kActColumns / 8, kSlots = kActThreads / kLanes;
+    __shared__ float part[kSlots][kActColumns];
+    __shared__ float cta_sum[kActColumns];
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = static_cast<int>(cluster.block_rank());
-    const int64_t col0 = static_cast<int64_t>(blockIdx.x / kActCluster) * kActSlab;
-    const int lane = threadIdx.x % (kActSlab / 8), slot = threadIdx.x / (kActSlab / 8);
+    const int64_t col0 = static_cast<int64_t>(blockIdx.x / kActCluster) * kActColumns;
+    const int lane = threadIdx.x % kLanes, slot = threadIdx.x / kLanes;
     const int64_t col = col0 + 8 * lane;
     float acc[8] = {};
     if (col < R) {
-        constexpr int kAhead = 2;  // rows in flight per thread
-        constexpr int64_t kStep = kActCluster * kActSlots;
-        for (int64_t t = rank * kActSlots + slot; t < T; t += kAhead * kStep) {
-            uint4 a[kAhead], b[kAhead];
+        for (int64_t t = rank * kSlots + slot; t < T; t += kActCluster * kSlots) {
+            float d[8], z[8];
+            widen<D>(*reinterpret_cast<const uint4 *>(dy + t * lddy + col), d);
+            widen<D>(*reinterpret_cast<const uint4 *>(pre + t * ldpre + col), z);
+            slopes(z, act);
 #pragma unroll
-            for (int u = 0; u < kAhead; u++)
-                if (t + u * kStep < T) {
-                    a[u] = *reinterpret_cast<const uint4 *>(dy + (t + u * kStep) * lddy + col);
-                    b[u] = *reinterpret_cast<const uint4 *>(pre + (t + u * kStep) * ldpre + col);
-                }
-#pragma unroll
-            for (int u = 0; u < kAhead; u++)
-                if (t + u * kStep < T) {
-                    float d[8], z[8];
-                    widen<D>(a[u], d);
-                    widen<D>(b[u], z);
-                    slopes(z, act);
-#pragma unroll
-                    for (int j = 0; j < 8; j++) {
-                        z[j] *= d[j];
-                        acc[j] += z[j];
-                    }
-                    *reinterpret_cast<uint4 *>(dz + (t + u * kStep) * lddz + col) = narrow<D>(z);
-                }
+            for (int j = 0; j < 8; j++) {
+                z[j] *= d[j];
+                acc[j] += z[j];
+            }
+            *reinterpret_cast<uint4 *>(dz + t * lddz + col) = narrow<D>(z);
         }
     }
+    if (!dbias)
+        return;  // the whole cluster
 #pragma unroll
     for (int j = 0; j < 8; j++)
         part[slot][8 * lane + j] = acc[j];
     __syncthreads();
-    if (threadIdx.x < kActSlab) {
+    if (threadIdx.x < kActColumns) {
         float s = 0.0f;
-        for (int i = 0; i < kActSlots; i++)
+#pragma unroll 8
+        for (int i = 0; i < kSlots; i++)
             s += part[i][threadIdx.x];
         cta_sum[threadIdx.x] = s;
     }
     cluster.sync();
-    if (rank == 0 && threadIdx.x < kActSlab && dbias && col0 + threadIdx.x < R) {
+    if (rank == 0 && threadIdx.x < kActColumns && col0 + threadIdx.x < R) {
         float s = 0.0f;
+#pragma unroll
         for (int i = 0; i < kActCluster; i++)
             s += cluster.map_shared_rank(cta_sum, i)[threadIdx.x];
         dbias[col0 + threadIdx.x] = s;
@@ -1128,8 +1123,8 @@ cq_status cq_activation_backward(const void *dy, int64_t lddy, const void *pre, 
         return CQ_OK;
     if (T > 0 && (!good_rows(dy, lddy, R) || !good_rows(pre, ldpre, R) || !good_rows(dz, lddz, R)))
         return CQ_ERR_INVALID_ARG;
-    const unsigned grid = static_cast<unsigned>((R + kActSlab - 1) / kActSlab * kActCluster);
     auto kernel = dtype == CQ_DTYPE_BF16 ? activation_backward_kernel<BF16> : activation_backward_kernel<FP16>;
+    const unsigned grid = static_cast<unsigned>((R + kActColumns - 1) / kActColumns * kActCluster);
     kernel<<<grid, kActThreads, 0, static_cast<cudaStream_t>(stream)>>>(
         static_cast<const uint16_t *>(dy), lddy, static_cast<const uint16_t *>(pre), ldpre, T, R, activation,
         static_cast<uint16_t *>(dz), lddz, dbias);

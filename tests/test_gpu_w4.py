@@ -93,6 +93,26 @@ def test_linear(T, R, K, dt):
     assert np.all(np.abs(f64(y0) - e0) <= linear_bound(x64, n, s, None, e0, e0, dt))
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_many_full_tiles(dt):
+    """Enough rows and outputs that every SM has several tiles of 256 tokens, with shared memory busy."""
+    from minimax_scale_search_b200 import cq
+    T, R, K = 4000, 4104, 2048
+    rng = np.random.default_rng(17)
+    w, n, s = make_layer(R, K, 17)
+    x, x64 = values(rng, (T, K), dt)
+    e = w4.linear(x64, n, s)[0]
+    bound = linear_bound(x64, n, s, None, e, e, dt)
+    for _ in range(3):
+        assert np.all(np.abs(f64(cq.w4_linear(x, w)) - e) <= bound)
+    dz, d64 = values(rng, (T, R), dt, 0.1)
+    edx, _ = w4.linear_backward(d64, x64, n, s)
+    A = np.abs(d64) @ np.abs(w4.weight(n, s))
+    bound = A * (U[dt] + (R + 8) * 2.0 ** -23) + U[dt] * np.abs(edx) + TINY[dt]
+    for _ in range(3):
+        assert np.all(np.abs(f64(cq.w4_linear_backward(dz, None, w, want_dscales=False)[0]) - edx) <= bound)
+
+
 @pytest.mark.parametrize("act", w4.ACTIVATIONS)
 @pytest.mark.parametrize("T", [3, 40])
 def test_activations_over_their_range(act, T):
@@ -321,18 +341,18 @@ def test_calls_are_deterministic():
             assert all(torch.equal(a, b) for a, b in zip(r, runs[0]))
 
 
-def _model(V=300, H=256, F=520, seed=0):
-    """A quantised table and two layers, by the framework's own selection and export."""
+def _model(V, H, F):
+    """A quantised table, a layer, and the table as a layer, by the framework's own selection and export."""
     import torch
     from minimax_scale_search_b200 import cq
-    gen = torch.Generator(device="cuda").manual_seed(seed)
+    gen = torch.Generator(device="cuda").manual_seed(0)
     made = []
-    for R, K in ((V, H), (F, H), (H, 640)):
+    for R, K in ((V, H), (F, H)):
         W = (0.05 * torch.randn((R, K), generator=gen, device="cuda")).half()
         D = torch.rand((2, K), generator=gen, device="cuda") + 0.1
         made.append(cq.select_scales(W, D))
     up = cq.w4_weights(cq.gptq_export(made[1].scales, made[1].codes, F, H))
-    head = cq.w4_weights(cq.gptq_export(made[0].scales, made[0].codes, V // 8 * 8, H)) if V % 8 == 0 else None
+    head = cq.w4_weights(cq.gptq_export(made[0].scales, made[0].codes, V, H))
     return made[0], up, head
 
 
