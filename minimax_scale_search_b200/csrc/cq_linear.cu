@@ -719,7 +719,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 constexpr int kGradN = 256;
 constexpr int kGradB = kGradN * kChunk * 2;
 constexpr int kGradStages = 4;
-constexpr int kSpan = 16;  // stages (1,024 tokens)
+constexpr int kSpan = 8;  // stages (512 tokens)
 constexpr int kGradThreads = 32 * 6;
 constexpr int kGradBytes = kGradStages * (kAStage + kGradB) + 8 * (2 * kGradStages + 4) + 16 + 1024;
 
@@ -780,7 +780,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                     const int64_t g = g0 + i;
                     if (g >= w.K / kGroup)
                         continue;
-                    const int z1 = inside ? static_cast<int>((w.qzeros[(g * w.R + r) / 8] >> (4 * (r & 7))) & 15u) + 1 : 0;
+                    const uint32_t zero = zero_pair<FP16>(inside ? (w.qzeros[(g * w.R + r) / 8] >> (4 * (r & 7))) & 15u : 0u);
                     float part = 0.0f;
                     for (int c = 0; c < kGroup; c += 32) {
                         uint32_t word[4], v[32];
@@ -790,9 +790,14 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                         __syncwarp();
                         tc::tmem_load32(tmem + (static_cast<uint32_t>(32 * warp) << 16) + sums.slot * kGradN + i * kGroup + c, v);
 #pragma unroll
-                        for (int j = 0; j < 32; j++)
-                            part = fmaf(__uint_as_float(v[j]),
-                                        static_cast<float>(static_cast<int>((word[j / 8] >> (4 * (j % 8))) & 15u) - z1), part);
+                        for (int j = 0; j < 4; j++)
+#pragma unroll
+                            for (int q = 0; q < 4; q++) {
+                                const uint32_t n = FP16::code_pair(word[j], q, zero, w.low);
+                                const float2 f = __half22float2(reinterpret_cast<const __half2 &>(n));
+                                part = fmaf(__uint_as_float(v[8 * j + q]), f.x, part);
+                                part = fmaf(__uint_as_float(v[8 * j + q + 4]), f.y, part);
+                            }
                     }
                     total[i] += part;
                 }
