@@ -355,6 +355,7 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
         const uint64_t b_first = tc::descriptor(base + kAStage, 16, 1024);
         const int64_t mine = static_cast<int64_t>(blockIdx.x) < tiles ? (tiles - 1 - blockIdx.x) / gridDim.x + 1 : 0;
         const uint32_t stages = static_cast<uint32_t>(2 * depth);
+        const bool leader = tc::elected();
         Ring<2> sums;
         uint32_t parity = 0, c = 0;
         int64_t left = mine;
@@ -374,17 +375,12 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
                 const uint64_t b = b_first + static_cast<uint32_t>(slot * (kAStage + S::kB) / 16);
                 const uint32_t d = tmem + sums.slot * N;
                 const bool last = ++c == stages;
-                if (tc::elected()) {
-                    tc::mma(d, a, b, kInstr, c > 1);
 #pragma unroll
-                    for (int k = 1; k < kChunk / 16; k++)
-                        tc::mma_add(d, a + k * (kStep / 16), b + k * (32 / 16), kInstr);
-                    tc::commit(empty(slot));
-                    if (last)
-                        tc::commit(sums_full(sums.slot));
-                }
-                __syncwarp();
+                for (int k = 0; k < kChunk / 16; k++)
+                    tc::mma(d, a + k * (kStep / 16), b + k * (32 / 16), kInstr, c > 1 || k > 0, leader);
+                tc::commit(empty(slot), leader);
                 if (last) {
+                    tc::commit(sums_full(sums.slot), leader);
                     c = 0;
                     sums.next();
                     if (--left == 0) {
@@ -837,6 +833,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     } else {
         constexpr uint32_t kInstr = tc::instruction(D::kMagic == BF16::kMagic, true, true, kGradN);
         const uint64_t a_first = tc::descriptor(base, 8192, 1024), b_first = tc::descriptor(base + kAStage, 8192, 1024);
+        const bool leader = tc::elected();
         Ring<kGradStages> op;
         Ring<2> sums;
         bool going = true;
@@ -852,19 +849,15 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                 const uint32_t d = tmem + sums.slot * kGradN;
                 const uint64_t a = a_first + static_cast<uint32_t>(op.slot * (kAStage + kGradB) / 16);
                 const uint64_t b = b_first + static_cast<uint32_t>(op.slot * (kAStage + kGradB) / 16);
-                if (tc::elected()) {
-                    tc::mma(d, a, b, kInstr, !first);
 #pragma unroll
-                    for (int k = 1; k < kChunk / 16; k++)
-                        tc::mma_add(d, a + k * 128, b + k * 128, kInstr);
-                    tc::commit(empty(op.slot));
-                    if (last)
-                        tc::commit(sums_full(sums.slot));
-                }
-                __syncwarp();
+                for (int k = 0; k < kChunk / 16; k++)
+                    tc::mma(d, a + k * 128, b + k * 128, kInstr, !first || k > 0, leader);
+                tc::commit(empty(op.slot), leader);
                 op.next();
-                if (last)
+                if (last) {
+                    tc::commit(sums_full(sums.slot), leader);
                     sums.next();
+                }
             }
         }
     }
