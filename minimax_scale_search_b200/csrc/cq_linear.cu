@@ -45,21 +45,23 @@ constexpr int kSetWords = kM * kChunk / 8 / (32 * kSetWarps);  // words of a sta
 constexpr int kCopyWarp = 4 + kUnpackWarps, kWordWarp = kCopyWarp + 1, kIssueWarp = kWordWarp + 1;
 constexpr int kTensorThreads = 32 * (kIssueWarp + 2);
 
-// Stages of (A, B) and of raw weights, by what 227 KB of shared memory hold.
+// Slots of unpacked weights (A), of activations (B) and of raw weights, by what 227 KB of shared memory hold.  Copies
+// take about 1,000 cycles from L2, a stage of few tokens under 300: their rings are the deeper, the smaller N is.
 template <int N>
 struct Stages {
     static constexpr int kB = N * kChunk * 2;
-    static constexpr int kOperands = N >= 128 ? 4 : 5;
-    static constexpr int kRaw = N >= 256 ? 4 : 16;
-    static constexpr int kBarriers = 2 * kOperands + 2 * kRaw + 4;
+    static constexpr int kASlots = 4;
+    static constexpr int kBSlots = N >= 256 ? 3 : N >= 128 ? 5 : N >= 64 ? 10 : 14;
+    static constexpr int kRaw = N >= 256 ? 8 : N >= 128 ? 8 : 12;
+    static constexpr int kBarriers = 2 * (kASlots + kBSlots + kRaw) + 4;
     static constexpr int kControl = 8 * kBarriers + 16;      // barriers, the stop flag, tensor memory's address
     static constexpr int kTurn = 4 * 16 * 33 * 4;            // the epilogue's turn from lanes to rows
-    static constexpr int kBytes = kOperands * (kAStage + kB) + kRaw * kRawStage + kControl + kTurn + 1024;
+    static constexpr int kBytes = kASlots * kAStage + kBSlots * kB + kRaw * kRawStage + kControl + kTurn + 1024;
     static constexpr int kColumns = 2 * N < 32 ? 32 : 2 * N;
     static_assert(kBytes <= 232448, "shared memory");
-    // A set that has filled stage c goes on to c + kUnpackSets.  It knows that c - kOperands has been read, and the
-    // parity of its next wait needs c + kUnpackSets - 2 kOperands to have been.
-    static_assert(kUnpackSets % 2 == 0 && kUnpackSets <= kOperands, "phases");
+    // A set that has filled stage c goes on to c + kUnpackSets.  It knows that c - kASlots has been read, and the
+    // parity of its next wait needs c + kUnpackSets - 2 kASlots to have been.
+    static_assert(kUnpackSets <= kASlots, "phases");
     // A slot of raw weights belongs to one set: loads complete in any order, so only the set that has read a slot
     // before knows which of its phases the next wait is for.
     static_assert(kRaw % kUnpackSets == 0, "phases");
@@ -165,14 +167,15 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
     extern __shared__ char shared_raw[];
     const uint32_t base = (tc::smem_address(shared_raw) + 1023) & ~1023u;
     char *shared = shared_raw + (base - tc::smem_address(shared_raw));
-    const uint32_t raw0 = base + S::kOperands * (kAStage + S::kB), bars = raw0 + S::kRaw * kRawStage;
-    auto a_at = [&](int i) { return base + i * (kAStage + S::kB); };
-    auto full = [&](int i) { return bars + 8 * i; };
-    auto empty = [&](int i) { return bars + 8 * (S::kOperands + i); };
-    auto raw_full = [&](int i) { return bars + 8 * (2 * S::kOperands + i); };
-    auto raw_empty = [&](int i) { return bars + 8 * (2 * S::kOperands + S::kRaw + i); };
-    auto sums_full = [&](int i) { return bars + 8 * (2 * S::kOperands + 2 * S::kRaw + i); };
-    auto sums_empty = [&](int i) { return bars + 8 * (2 * S::kOperands + 2 * S::kRaw + 2 + i); };
+    const uint32_t b0 = base + S::kASlots * kAStage, raw0 = b0 + S::kBSlots * S::kB, bars = raw0 + S::kRaw * kRawStage;
+    auto a_full = [&](int i) { return bars + 8 * i; };
+    auto a_empty = [&](int i) { return bars + 8 * (S::kASlots + i); };
+    auto b_full = [&](int i) { return bars + 8 * (2 * S::kASlots + i); };
+    auto b_empty = [&](int i) { return bars + 8 * (2 * S::kASlots + S::kBSlots + i); };
+    auto raw_full = [&](int i) { return bars + 8 * (2 * (S::kASlots + S::kBSlots) + i); };
+    auto raw_empty = [&](int i) { return bars + 8 * (2 * (S::kASlots + S::kBSlots) + S::kRaw + i); };
+    auto sums_full = [&](int i) { return bars + 8 * (2 * (S::kASlots + S::kBSlots + S::kRaw) + i); };
+    auto sums_empty = [&](int i) { return bars + 8 * (2 * (S::kASlots + S::kBSlots + S::kRaw) + 2 + i); };
     volatile int *stop = reinterpret_cast<volatile int *>(shared + (bars - base) + 8 * S::kBarriers);
     uint32_t *tmem_at = const_cast<uint32_t *>(reinterpret_cast<volatile uint32_t *>(stop + 1));
 
@@ -183,9 +186,13 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
     if (warp == kIssueWarp)
         tc::tmem_alloc(tc::smem_address(tmem_at), S::kColumns);
     if (threadIdx.x == 0) {
-        for (int i = 0; i < S::kOperands; i++) {
-            tc::barrier_init(full(i), kSetWarps + 1);
-            tc::barrier_init(empty(i), 1);
+        for (int i = 0; i < S::kASlots; i++) {
+            tc::barrier_init(a_full(i), kSetWarps);
+            tc::barrier_init(a_empty(i), 1);
+        }
+        for (int i = 0; i < S::kBSlots; i++) {
+            tc::barrier_init(b_full(i), 1);
+            tc::barrier_init(b_empty(i), 1);
         }
         for (int i = 0; i < S::kRaw; i++) {
             tc::barrier_init(raw_full(i), 32 + 1);
@@ -273,7 +280,7 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
         const int64_t stages = (static_cast<int64_t>(blockIdx.x) < tiles ? (tiles - 1 - blockIdx.x) / gridDim.x + 1 : 0) * 2 * depth;
         int raw = set;
         uint32_t raw_parity = 0;
-        Ring<S::kOperands> op;
+        Ring<S::kASlots> op;
         op.skip(set);
         for (int64_t c = set; c < stages; c += kUnpackSets) {
             if (!tc::barrier_wait_warp(raw_full(raw), raw_parity, stop))
@@ -290,9 +297,9 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
 #pragma unroll
             for (int j = 0; j < kSetWords; j++)
                 values[j] = unpack(word[j], w.low);
-            if (!tc::barrier_wait_warp(empty(op.slot), op.parity ^ 1, stop))
+            if (!tc::barrier_wait_warp(a_empty(op.slot), op.parity ^ 1, stop))
                 break;
-            char *to = shared + (a_at(op.slot) - base) + a;
+            char *to = shared + op.slot * kAStage + a;
 #pragma unroll
             for (int j = 0; j < kSetWords; j++)
                 *reinterpret_cast<uint4 *>(to + (((k8 + j) & 7) ^ (r & 7)) * 16) = values[j];
@@ -302,7 +309,7 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
             // shared loads in flight, and with shared memory busy the next words overtook them.
             if (lane == 0) {
                 tc::barrier_arrive(raw_empty(raw));
-                tc::barrier_arrive(full(op.slot));
+                tc::barrier_arrive(a_full(op.slot));
             }
             raw += kUnpackSets;
             if (raw >= S::kRaw) {
@@ -312,17 +319,17 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
             op.skip(kUnpackSets);
         }
     } else if (warp == kCopyWarp) {  // activations, by tensor map
-        Ring<S::kOperands> op;
+        Ring<S::kBSlots> op;
         bool going = true;
         for (int64_t tile = blockIdx.x; going && tile < tiles; tile += gridDim.x) {
             const int t0 = static_cast<int>(tile % tiles_n * N), end = static_cast<int>(2 * depth) * kChunk;
             for (int c = 0; c < end; c += kChunk) {
-                going = tc::barrier_wait_warp(empty(op.slot), op.parity ^ 1, stop);
+                going = tc::barrier_wait_warp(b_empty(op.slot), op.parity ^ 1, stop);
                 if (!going)
                     break;
                 if (tc::elected()) {
-                    tc::barrier_expect(full(op.slot), S::kB);
-                    tc::copy_box(a_at(op.slot) + kAStage, &act_map, c, t0, full(op.slot));
+                    tc::barrier_expect(b_full(op.slot), S::kB);
+                    tc::copy_box(b0 + op.slot * S::kB, &act_map, c, t0, b_full(op.slot));
                 }
                 __syncwarp();
                 op.next();
@@ -352,44 +359,34 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
         constexpr uint32_t kInstr = tc::instruction(D::kMagic == BF16::kMagic, kGradient, false, N);
         constexpr uint32_t kStep = kGradient ? 2048 : 32;  // 16 of the contraction in A: 16 rows, or 32 bytes of a row
         const uint64_t a_first = tc::descriptor(base, kGradient ? kAStage / 2 : 16, 1024);
-        const uint64_t b_first = tc::descriptor(base + kAStage, 16, 1024);
-        const int64_t mine = static_cast<int64_t>(blockIdx.x) < tiles ? (tiles - 1 - blockIdx.x) / gridDim.x + 1 : 0;
-        const uint32_t stages = static_cast<uint32_t>(2 * depth);
+        const uint64_t b_first = tc::descriptor(b0, 16, 1024);
         const bool leader = tc::elected();
+        Ring<S::kASlots> a_ring;
+        Ring<S::kBSlots> b_ring;
         Ring<2> sums;
-        uint32_t parity = 0, c = 0;
-        int64_t left = mine;
-        bool going = left > 0;
-        while (going) {
-#pragma unroll
-            for (int slot = 0; slot < S::kOperands; slot++) {  // unrolled: addresses and descriptors stay fixed
-                if (c == 0) {
-                    going = going && tc::barrier_wait_warp(sums_empty(sums.slot), sums.parity ^ 1, stop);
-                    tc::fence_after();
-                }
-                going = going && tc::barrier_wait_warp(full(slot), parity, stop);
+        bool going = true;
+        for (int64_t tile = blockIdx.x; going && tile < tiles; tile += gridDim.x) {
+            going = tc::barrier_wait_warp(sums_empty(sums.slot), sums.parity ^ 1, stop);
+            const uint32_t d = tmem + sums.slot * N;
+            for (int c = 0; going && c < static_cast<int>(2 * depth); c++) {
+                going = tc::barrier_wait_warp(b_full(b_ring.slot), b_ring.parity, stop) &&
+                        tc::barrier_wait_warp(a_full(a_ring.slot), a_ring.parity, stop);
                 if (!going)
                     break;
                 tc::fence_after();
-                const uint64_t a = a_first + static_cast<uint32_t>(slot * (kAStage + S::kB) / 16);
-                const uint64_t b = b_first + static_cast<uint32_t>(slot * (kAStage + S::kB) / 16);
-                const uint32_t d = tmem + sums.slot * N;
-                const bool last = ++c == stages;
+                const uint64_t a = a_first + static_cast<uint32_t>(a_ring.slot * (kAStage / 16));
+                const uint64_t b = b_first + static_cast<uint32_t>(b_ring.slot * (S::kB / 16));
 #pragma unroll
                 for (int k = 0; k < kChunk / 16; k++)
-                    tc::mma(d, a + k * (kStep / 16), b + k * (32 / 16), kInstr, c > 1 || k > 0, leader);
-                tc::commit(empty(slot), leader);
-                if (last) {
-                    tc::commit(sums_full(sums.slot), leader);
-                    c = 0;
-                    sums.next();
-                    if (--left == 0) {
-                        going = false;
-                        break;
-                    }
-                }
+                    tc::mma(d, a + k * (kStep / 16), b + k * (32 / 16), kInstr, c > 0 || k > 0, leader);
+                tc::commit(a_empty(a_ring.slot), leader);
+                tc::commit(b_empty(b_ring.slot), leader);
+                a_ring.next();
+                b_ring.next();
             }
-            parity ^= 1;
+            if (going)
+                tc::commit(sums_full(sums.slot), leader);
+            sums.next();
         }
     } else {  // half the lanes 16 bytes (8 outputs) of scales, half a word of zero points
         Ring<S::kRaw> raw;
