@@ -241,7 +241,7 @@ cq_status cq_gptq_dequantize(const int32_t *qweight, const int32_t *qzeros, cons
 #define CQ_ACT_SILU 4      /* z / (1 + exp(-z)) */
 
 /* Linear layer: z = x W^T + bias, y = act(z) + residual.
- *  x         [T][K], ldx.           bias      [R] of dtype, nullable.
+ *  x         [T][K], ldx.           bias      [R] of dtype, nullable, 16-byte aligned.
  *  residual  [T][R], ldres, nullable; may be y itself (with ldres == ldy).
  *  y         [T][R], ldy.           pre       [T][R], ldpre, nullable: z, for the backward pass.
  * x is multiplied by W; up to CQ_W4_EXACT_ROWS rows with W's exact values (integers in the

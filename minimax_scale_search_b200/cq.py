@@ -629,7 +629,7 @@ def w4_linear(x, w: W4Weights, *, bias=None, activation: str = "none", residual=
     """y = activation(x W^T + bias) + residual, W the layer's 4-bit weights.
 
     x: [T, K] bfloat16 or float16, rows contiguous (they may be strided) and
-       16-byte aligned; bias [R], residual [T, R] of x's type.  ``out`` may be
+       16-byte aligned; bias [R] (16-byte aligned), residual [T, R] of x's type.  ``out`` may be
        the residual itself.  activation: one of ACTIVATIONS.
        Returns y [T, R], or (y, pre) with ``want_pre``: pre = x W^T + bias, which
        activation_backward takes."""
@@ -638,8 +638,8 @@ def w4_linear(x, w: W4Weights, *, bias=None, activation: str = "none", residual=
     T, R, K = x.shape[0], w.R, w.K
     ldx = _rows16("x", x, T, K, x)
     if bias is not None and (bias.shape != (R,) or bias.dtype != x.dtype or bias.device != x.device or
-                             not bias.is_contiguous()):
-        raise ValueError(f"bias must be a contiguous {x.dtype} [{R}] tensor on {x.device}")
+                             not bias.is_contiguous() or bias.data_ptr() % 16):
+        raise ValueError(f"bias must be a contiguous 16-byte aligned {x.dtype} [{R}] tensor on {x.device}")
     ldres = _rows16("residual", residual, T, R, x) if residual is not None else 0
     handle, context = _place(x.device, stream)
     if out is None:

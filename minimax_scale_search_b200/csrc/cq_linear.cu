@@ -1,6 +1,8 @@
 // Linear layers on 4-bit weights, and their gradients.
 #include <cooperative_groups.h>
 
+#include <utility>
+
 #include "cq_tensor.cuh"
 #include "cq_w4.cuh"
 
@@ -32,7 +34,8 @@ struct Layer {
 //
 // Warps: 0-3 epilogue, 4-19 unpack, then one each that copies activations, copies words, issues the matrix
 // instructions, copies scales and zero points.  CTAs are persistent; two accumulators in tensor memory let
-// a tile's epilogue run under the next tile's products.
+// a tile's epilogue run under the next tile's products.  Where there are too few tiles for the SMs, a cluster shares
+// a tile's contraction and adds its sums up through distributed shared memory, in the order of its ranks.
 
 constexpr int kM = 128;
 constexpr int kChunk = 64;                     // contraction per stage
@@ -158,6 +161,25 @@ struct Ring {
     }
 };
 
+// z of eight adjacent m of one token -> pre, y.
+template <class D, bool kGradient>
+__device__ __forceinline__ void finish_row(const Epilogue &ep, int64_t t, int64_t m, float (&z)[8], const uint4 &res)
+{
+    if (!kGradient) {
+        if (ep.pre)
+            *reinterpret_cast<uint4 *>(ep.pre + t * ep.ldpre + m) = narrow<D>(z);
+        activate(z, ep.act);
+        if (ep.res) {
+            float r[8];
+            widen<D>(res, r);
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                z[j] += r[j];
+        }
+    }
+    *reinterpret_cast<uint4 *>(ep.y + t * ep.ldy + m) = narrow<D>(z);
+}
+
 template <class D, int N, bool kGradient>
 __global__ void __launch_bounds__(kTensorThreads, 1)
     weights_product_kernel(const __grid_constant__ CUtensorMap act_map, const __grid_constant__ CUtensorMap word_map,
@@ -180,8 +202,13 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
     uint32_t *tmem_at = const_cast<uint32_t *>(reinterpret_cast<volatile uint32_t *>(stop + 1));
 
     const int warp = tc::uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
-    const int64_t rows = kGradient ? w.K : w.R, depth = kGradient ? (w.R + kM - 1) / kM : w.K / kM;  // in steps of 128
+    // a cluster shares the tile's contraction: this CTA has `depth` steps of 128 of it, from `first`
+    cg::cluster_group cluster = cg::this_cluster();
+    const int ranks = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+    const int64_t rows = kGradient ? w.K : w.R, steps = kGradient ? (w.R + kM - 1) / kM : w.K / kM;
+    const int first = static_cast<int>(steps * rank / ranks), depth = static_cast<int>(steps * (rank + 1) / ranks) - first;
     const int64_t tiles_n = (T + N - 1) / N, tiles = (rows + kM - 1) / kM * tiles_n;
+    const int64_t tile0 = blockIdx.x / ranks, tile_step = gridDim.x / ranks;
 
     if (warp == kIssueWarp)
         tc::tmem_alloc(tc::smem_address(tmem_at), S::kColumns);
@@ -220,7 +247,7 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
         float *turn = reinterpret_cast<float *>(shared + (bars - base) + S::kControl) + warp * (16 * 33);
         Ring<2> sums;
         const int tok = lane >> 2, part = 8 * (lane & 3);
-        for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        for (int64_t tile = tile0; tile < tiles; tile += tile_step) {
             const int64_t m0 = tile / tiles_n * kM + 32 * warp, t0 = tile % tiles_n * N, m = m0 + part;
             const float bias = ep.bias && m0 + lane < rows ? D::to_float(ep.bias[m0 + lane]) : 0.0f;
             const int64_t left = T - t0;
@@ -228,6 +255,17 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
             if (!tc::barrier_wait_warp(sums_full(sums.slot), sums.parity, stop))
                 break;
             tc::fence_after();
+            if (ranks > 1) {  // the sums go to shared memory, [token][m], for the cluster
+                float *to = reinterpret_cast<float *>(shared) + 32 * warp + lane;
+                for (int c = 0; c < tokens; c += 16) {
+                    uint32_t v[16];
+                    tc::tmem_load16(tmem + (static_cast<uint32_t>(32 * warp) << 16) + sums.slot * N + c, v);
+#pragma unroll
+                    for (int j = 0; j < 16; j++)
+                        to[(c + j) * kM] = __uint_as_float(v[j]);
+                }
+                break;
+            }
             for (int c = 0; c < tokens; c += 16) {
                 uint4 res[2];
 #pragma unroll
@@ -250,19 +288,7 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 8; j++)
                         z[j] = turn[(8 * h + tok) * 33 + part + j];
-                    if (!kGradient) {
-                        if (ep.pre)
-                            *reinterpret_cast<uint4 *>(ep.pre + t * ep.ldpre + m) = narrow<D>(z);
-                        activate(z, ep.act);
-                        if (ep.res) {
-                            float r[8];
-                            widen<D>(res[h], r);
-#pragma unroll
-                            for (int j = 0; j < 8; j++)
-                                z[j] += r[j];
-                        }
-                    }
-                    *reinterpret_cast<uint4 *>(ep.y + t * ep.ldy + m) = narrow<D>(z);
+                    finish_row<D, kGradient>(ep, t, m, z, res[h]);
                 }
             }
             tc::fence_before();
@@ -277,7 +303,7 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
         constexpr int kOutputs = kGradient ? 64 : kM;       // outputs of a stage
         const int r = i % kOutputs, k8 = i / kOutputs * kSetWords;  // output and first word row within it
         const uint32_t a = kGradient ? (k8 >> 3) * (kAStage / 2) + r * 128 : r * 128;
-        const int64_t stages = (static_cast<int64_t>(blockIdx.x) < tiles ? (tiles - 1 - blockIdx.x) / gridDim.x + 1 : 0) * 2 * depth;
+        const int64_t stages = (tile0 < tiles ? (tiles - 1 - tile0) / tile_step + 1 : 0) * 2 * depth;
         int raw = set;
         uint32_t raw_parity = 0;
         Ring<S::kASlots> op;
@@ -321,9 +347,9 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
     } else if (warp == kCopyWarp) {  // activations, by tensor map
         Ring<S::kBSlots> op;
         bool going = true;
-        for (int64_t tile = blockIdx.x; going && tile < tiles; tile += gridDim.x) {
-            const int t0 = static_cast<int>(tile % tiles_n * N), end = static_cast<int>(2 * depth) * kChunk;
-            for (int c = 0; c < end; c += kChunk) {
+        for (int64_t tile = tile0; going && tile < tiles; tile += tile_step) {
+            const int t0 = static_cast<int>(tile % tiles_n * N), end = (first + depth) * kM;
+            for (int c = first * kM; c < end; c += kChunk) {
                 going = tc::barrier_wait_warp(b_empty(op.slot), op.parity ^ 1, stop);
                 if (!going)
                     break;
@@ -338,10 +364,10 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
     } else if (warp == kWordWarp) {  // words, by tensor map
         Ring<S::kRaw> raw;
         bool going = true;
-        for (int64_t tile = blockIdx.x; going && tile < tiles; tile += gridDim.x) {
+        for (int64_t tile = tile0; going && tile < tiles; tile += tile_step) {
             const int m0 = static_cast<int>(tile / tiles_n * kM);
-            int r = kGradient ? 0 : m0, row = kGradient ? m0 / 8 : 0;
-            for (int c = 0; c < static_cast<int>(2 * depth); c++) {
+            int r = kGradient ? first * kM : m0, row = kGradient ? m0 / 8 : first * kWordsPerGroup;
+            for (int c = 0; c < 2 * depth; c++) {
                 going = tc::barrier_wait_warp(raw_empty(raw.slot), raw.parity ^ 1, stop);
                 if (!going)
                     break;
@@ -365,10 +391,10 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
         Ring<S::kBSlots> b_ring;
         Ring<2> sums;
         bool going = true;
-        for (int64_t tile = blockIdx.x; going && tile < tiles; tile += gridDim.x) {
+        for (int64_t tile = tile0; going && tile < tiles; tile += tile_step) {
             going = tc::barrier_wait_warp(sums_empty(sums.slot), sums.parity ^ 1, stop);
             const uint32_t d = tmem + sums.slot * N;
-            for (int c = 0; going && c < static_cast<int>(2 * depth); c++) {
+            for (int c = 0; going && c < 2 * depth; c++) {
                 going = tc::barrier_wait_warp(b_full(b_ring.slot), b_ring.parity, stop) &&
                         tc::barrier_wait_warp(a_full(a_ring.slot), a_ring.parity, stop);
                 if (!going)
@@ -395,13 +421,13 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
         const bool mine = !kGradient || l < 8;
         const int64_t group_step = lane < 16 ? 2 * w.R : w.R / 2;
         bool going = true;
-        for (int64_t tile = blockIdx.x; going && tile < tiles; tile += gridDim.x) {
+        for (int64_t tile = tile0; going && tile < tiles; tile += tile_step) {
             const int64_t m0 = tile / tiles_n * kM;
-            int64_t r = (kGradient ? 0 : m0) + 8 * l;
-            const int64_t group = kGradient ? m0 / kGroup : 0;
+            int64_t r = (kGradient ? static_cast<int64_t>(first) * kM : m0) + 8 * l;
+            const int64_t group = kGradient ? m0 / kGroup : first;
             const char *from = lane < 16 ? reinterpret_cast<const char *>(w.scales + group * w.R + r)
                                          : reinterpret_cast<const char *>(w.qzeros + (group * w.R + r) / 8);
-            for (int c = 0; c < static_cast<int>(2 * depth); c++) {
+            for (int c = 0; c < 2 * depth; c++) {
                 going = tc::barrier_wait_warp(raw_empty(raw.slot), raw.parity ^ 1, stop);
                 if (!going)
                     break;
@@ -432,7 +458,40 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
     }
     if (warp == kIssueWarp)
         tc::tmem_free(tmem, S::kColumns);
+    if (ranks == 1)
+        return;
+    // the cluster's sums, each CTA a part of the tile's rows, in the order of the ranks
+    cluster.sync();
+    const int64_t m0 = tile0 / tiles_n * kM, t0 = tile0 % tiles_n * N, left = T - t0;
+    const int items = (left < N ? static_cast<int>(left) : N) * (kM / 8);
+    for (int i = rank * kTensorThreads + threadIdx.x; i < items; i += ranks * kTensorThreads) {
+        const int64_t t = t0 + i / (kM / 8), m = m0 + i % (kM / 8) * 8;
+        if (m >= rows)
+            continue;
+        float z[8] = {};
+#pragma unroll
+        for (int k = 0; k < 8; k++)
+            if (k < ranks) {
+                const float4 *from = reinterpret_cast<const float4 *>(cluster.map_shared_rank(reinterpret_cast<float *>(shared), k)) + 2 * i;
+                const float4 a = from[0], b = from[1];
+                z[0] += a.x; z[1] += a.y; z[2] += a.z; z[3] += a.w;
+                z[4] += b.x; z[5] += b.y; z[6] += b.z; z[7] += b.w;
+            }
+        if (!kGradient && ep.bias) {
+            float b[8];
+            widen<D>(*reinterpret_cast<const uint4 *>(ep.bias + m), b);
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                z[j] += b[j];
+        }
+        uint4 res = make_uint4(0, 0, 0, 0);
+        if (!kGradient && ep.res)
+            res = *reinterpret_cast<const uint4 *>(ep.res + t * ep.ldres + m);
+        finish_row<D, kGradient>(ep, t, m, z, res);
+    }
+    cluster.sync();  // peers keep their shared memory until it has been read
 }
+
 
 // ---- few rows ----------------------------------------------------------------------------------
 //
@@ -947,8 +1006,25 @@ CUtensorMapDataType map_type()
     return D::kMagic == BF16::kMagic ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
 }
 
+template <class... P, class... A>
+cq_status launch_clusters(void (*kernel)(P...), int64_t ctas, int ranks, int threads, int bytes, cudaStream_t stream, A &&...args)
+{
+    cudaLaunchConfig_t config = {};
+    config.gridDim = dim3(static_cast<unsigned>(ctas));
+    config.blockDim = dim3(threads);
+    config.dynamicSmemBytes = bytes;
+    config.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(ranks);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    config.attrs = attr;
+    config.numAttrs = 1;
+    return cudaLaunchKernelEx(&config, kernel, std::forward<A>(args)...) == cudaSuccess ? CQ_OK : CQ_ERR_CUDA;
+}
+
 template <class D, int N, bool kGradient>
-cq_status run_product(const uint16_t *act, int64_t ld, int64_t T, const Layer &w, const Epilogue &ep, cudaStream_t stream)
+cq_status run_product(const uint16_t *act, int64_t ld, int64_t T, const Layer &w, const Epilogue &ep, int ranks, cudaStream_t stream)
 {
     CUtensorMap act_map, word_map;
     const int64_t rows = kGradient ? w.K : w.R;
@@ -960,29 +1036,36 @@ cq_status run_product(const uint16_t *act, int64_t ld, int64_t T, const Layer &w
     if (allow_shared<kernel>(Stages<N>::kBytes) != cudaSuccess)
         return CQ_ERR_CUDA;
     const int64_t tiles = (rows + kM - 1) / kM * ((T + N - 1) / N), sms = sm_count();
-    kernel<<<static_cast<unsigned>(tiles < sms ? tiles : sms), kTensorThreads, Stages<N>::kBytes, stream>>>(act_map, word_map, w, T, ep);
-    return launched();
+    return launch_clusters(kernel, ranks > 1 ? tiles * ranks : tiles < sms ? tiles : sms, ranks, kTensorThreads, Stages<N>::kBytes,
+                           stream, act_map, word_map, w, T, ep);
 }
 
-// Tokens per tile: the least time by a count of waves, a stage of N tokens costing 2 N cycles on the tensor
-// core but never less than about 450, what the chain of waits between the warps takes.
+// Tokens per tile and CTAs per tile: the least time by a count of waves.  A stage of N tokens costs 2 N cycles on the
+// tensor core but never less than about 400, what the chain of waits between the warps takes; a tile about 3,000 more to start
+// and to end, a cluster's sums 2,000 and a few for each token.
 template <class D, bool kGradient>
 cq_status product(const uint16_t *act, int64_t ld, int64_t T, const Layer &w, const Epilogue &ep, cudaStream_t stream)
 {
-    const int64_t m = ((kGradient ? w.K : w.R) + kM - 1) / kM, sms = sm_count();
+    const int64_t m = ((kGradient ? w.K : w.R) + kM - 1) / kM, steps = kGradient ? (w.R + kM - 1) / kM : w.K / kM, sms = sm_count();
     int64_t least = INT64_MAX;
-    int best = 256;
-    for (int n = 256; n >= 32; n /= 2) {
-        const int64_t waves = (m * ((T + n - 1) / n) + sms - 1) / sms, cost = waves * (2 * n > 450 ? 2 * n : 450);
-        if (cost < least) {
-            least = cost;
-            best = n;
+    int best = 256, ranks = 1;
+    for (int n = 256; n >= 32; n /= 2)
+        for (int r = 1; r <= 8 && r <= steps; r *= 2) {
+            const int64_t tiles = m * ((T + n - 1) / n);
+            if (r > 1 && tiles * r > sms)
+                break;
+            const int64_t waves = (tiles * r + sms - 1) / sms, stage = 2 * n > 400 ? 2 * n : 400;
+            const int64_t cost = waves * 2 * ((steps + r - 1) / r) * stage + 3000 + (r > 1 ? 2000 + 8 * n : 0);
+            if (cost < least) {
+                least = cost;
+                best = n;
+                ranks = r;
+            }
         }
-    }
-    return best == 256   ? run_product<D, 256, kGradient>(act, ld, T, w, ep, stream)
-           : best == 128 ? run_product<D, 128, kGradient>(act, ld, T, w, ep, stream)
-           : best == 64  ? run_product<D, 64, kGradient>(act, ld, T, w, ep, stream)
-                         : run_product<D, 32, kGradient>(act, ld, T, w, ep, stream);
+    return best == 256   ? run_product<D, 256, kGradient>(act, ld, T, w, ep, ranks, stream)
+           : best == 128 ? run_product<D, 128, kGradient>(act, ld, T, w, ep, ranks, stream)
+           : best == 64  ? run_product<D, 64, kGradient>(act, ld, T, w, ep, ranks, stream)
+                         : run_product<D, 32, kGradient>(act, ld, T, w, ep, ranks, stream);
 }
 
 // CTAs per cluster: the least number of groups in a row on an SM, a CTA costing about eight groups more
@@ -1006,18 +1089,8 @@ cq_status few_rows(const uint16_t *x, int64_t ldx, int64_t T, const Layer &w, co
     constexpr auto kernel = few_rows_kernel<D, NT>;
     if (allow_shared<kernel>(FewStages<NT>::kBytes) != cudaSuccess)
         return CQ_ERR_CUDA;
-    cudaLaunchConfig_t config = {};
-    config.gridDim = dim3(static_cast<unsigned>(tiles * ranks));
-    config.blockDim = dim3(kFewThreads);
-    config.dynamicSmemBytes = FewStages<NT>::kBytes;
-    config.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(ranks);
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    config.attrs = attr;
-    config.numAttrs = 1;
-    return cudaLaunchKernelEx(&config, kernel, word_map, x, ldx, static_cast<int>(T), w, ep) == cudaSuccess ? CQ_OK : CQ_ERR_CUDA;
+    return launch_clusters(kernel, tiles * ranks, ranks, kFewThreads, FewStages<NT>::kBytes, stream, word_map, x, ldx,
+                           static_cast<int>(T), w, ep);
 }
 
 template <class D>
@@ -1067,7 +1140,7 @@ cq_status cq_w4_linear(const void *x, int64_t ldx, int dtype, int64_t T, const i
     if (T == 0 || R == 0)
         return CQ_OK;
     if (!good_rows(x, ldx, K) || !good_rows(y, ldy, R) || (residual && !good_rows(residual, ldres, R)) ||
-        (pre && !good_rows(pre, ldpre, R)) || (bias && !is_aligned(bias, 2)))
+        (pre && !good_rows(pre, ldpre, R)) || (bias && !is_aligned(bias, 16)))
         return CQ_ERR_INVALID_ARG;
     const Layer w = {reinterpret_cast<const uint32_t *>(qweight), reinterpret_cast<const uint32_t *>(qzeros), gptq_scales, R, K, kLow};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
