@@ -62,11 +62,8 @@ struct Stages {
     static constexpr int kBytes = kASlots * kAStage + kBSlots * kB + kRaw * kRawStage + kControl + kTurn + 1024;
     static constexpr int kColumns = 2 * N < 32 ? 32 : 2 * N;
     static_assert(kBytes <= 232448, "shared memory");
-    // A set that has filled stage c goes on to c + kUnpackSets.  It knows that c - kASlots has been read, and the
-    // parity of its next wait needs c + kUnpackSets - 2 kASlots to have been.
-    static_assert(kUnpackSets <= kASlots, "phases");
-    // A slot of raw weights belongs to one set: loads complete in any order, so only the set that has read a slot
-    // before knows which of its phases the next wait is for.
+    // A slot of raw weights belongs to one set, as a slot of A does: loads complete in any order, so only the set that
+    // has read a slot before knows which of its phases the next wait is for.
     static_assert(kRaw % kUnpackSets == 0, "phases");
 };
 
@@ -298,51 +295,51 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
             sums.next();
         }
     } else if (warp < 4 + kUnpackWarps) {  // unpack
-        // Sets of warps take the stages in turn.
+        // Sets of warps take the stages in turn, each with its slot of A: a word row of eight a thread.
+        static_assert(kSetWords == 8 && kUnpackSets == S::kASlots, "a set fills the same slot each time");
         const int i = threadIdx.x % (32 * kSetWarps), set = (warp - 4) / kSetWarps;
         constexpr int kOutputs = kGradient ? 64 : kM;       // outputs of a stage
         const int r = i % kOutputs, k8 = i / kOutputs * kSetWords;  // output and first word row within it
-        const uint32_t a = kGradient ? (k8 >> 3) * (kAStage / 2) + r * 128 : r * 128;
-        const int64_t stages = (tile0 < tiles ? (tiles - 1 - tile0) / tile_step + 1 : 0) * 2 * depth;
+        const uint32_t to = (base + set * kAStage + (k8 >> 3) * (kAStage / 2) + r * 128) | (r & 7) << 4;  // chunk j lies at ^ j << 4
+        const uint32_t full = a_full(set), empty = a_empty(set);
+        const int zero_shift = 4 * (r & 7);
+        uint32_t parity = 1, raw_parity = 0;
         int raw = set;
-        uint32_t raw_parity = 0;
-        Ring<S::kASlots> op;
-        op.skip(set);
-        for (int64_t c = set; c < stages; c += kUnpackSets) {
+        int64_t left = ((tile0 < tiles ? (tiles - 1 - tile0) / tile_step + 1 : 0) * 2 * depth - set + kUnpackSets - 1) / kUnpackSets;
+        for (; left > 0; left--) {
             if (!tc::barrier_wait_warp(raw_full(raw), raw_parity, stop))
                 break;
             const char *slot = shared + (raw0 - base) + raw * kRawStage;
             const uint32_t *words = reinterpret_cast<const uint32_t *>(slot) + k8 * kOutputs + r;
-            const Unpack<D> unpack(reinterpret_cast<const uint16_t *>(slot + kRawWords)[r],
-                                   (reinterpret_cast<const uint32_t *>(slot + kRawWords + 256)[r >> 3] >> (4 * (r & 7))) & 15u);
             uint32_t word[kSetWords];
 #pragma unroll
             for (int j = 0; j < kSetWords; j++)
                 word[j] = words[j * kOutputs];
+            const Unpack<D> unpack(reinterpret_cast<const uint16_t *>(slot + kRawWords)[r],
+                                   (reinterpret_cast<const uint32_t *>(slot + kRawWords + 256)[r >> 3] >> zero_shift) & 15u);
             uint4 values[kSetWords];
 #pragma unroll
             for (int j = 0; j < kSetWords; j++)
                 values[j] = unpack(word[j], w.low);
-            if (!tc::barrier_wait_warp(a_empty(op.slot), op.parity ^ 1, stop))
+            if (!tc::barrier_wait_warp(empty, parity, stop))
                 break;
-            char *to = shared + op.slot * kAStage + a;
 #pragma unroll
             for (int j = 0; j < kSetWords; j++)
-                *reinterpret_cast<uint4 *>(to + (((k8 + j) & 7) ^ (r & 7)) * 16) = values[j];
+                tc::store_shared(to ^ j << 4, values[j]);
             tc::fence_shared_writes();
             __syncwarp();
             // The words are released only here, after stores that needed them: an arrival does not wait for
             // shared loads in flight, and with shared memory busy the next words overtook them.
             if (lane == 0) {
                 tc::barrier_arrive(raw_empty(raw));
-                tc::barrier_arrive(a_full(op.slot));
+                tc::barrier_arrive(full);
             }
+            parity ^= 1;
             raw += kUnpackSets;
             if (raw >= S::kRaw) {
                 raw -= S::kRaw;
                 raw_parity ^= 1;
             }
-            op.skip(kUnpackSets);
         }
     } else if (warp == kCopyWarp) {  // activations, by tensor map
         Ring<S::kBSlots> op;
@@ -395,8 +392,7 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
             going = tc::barrier_wait_warp(sums_empty(sums.slot), sums.parity ^ 1, stop);
             const uint32_t d = tmem + sums.slot * N;
             for (int c = 0; going && c < 2 * depth; c++) {
-                going = tc::barrier_wait_warp(b_full(b_ring.slot), b_ring.parity, stop) &&
-                        tc::barrier_wait_warp(a_full(a_ring.slot), a_ring.parity, stop);
+                going = tc::barrier_wait_both(b_full(b_ring.slot), b_ring.parity, a_full(a_ring.slot), a_ring.parity, stop);
                 if (!going)
                     break;
                 tc::fence_after();
@@ -1056,7 +1052,7 @@ cq_status product(const uint16_t *act, int64_t ld, int64_t T, const Layer &w, co
                 break;
             const int64_t waves = (tiles * r + sms - 1) / sms, stage = 2 * n > 400 ? 2 * n : 400;
             const int64_t cost = waves * 2 * ((steps + r - 1) / r) * stage + 3000 + (r > 1 ? 2000 + 8 * n : 0);
-            if (cost < least) {
+            if (cost <= least) {  // of equals the smallest tile
                 least = cost;
                 best = n;
                 ranks = r;

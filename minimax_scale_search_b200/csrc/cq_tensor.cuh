@@ -99,6 +99,15 @@ __device__ __forceinline__ bool barrier_wait_warp(uint32_t bar, uint32_t parity,
     return __all_sync(0xFFFFFFFFu, barrier_wait(bar, parity, stop));
 }
 
+// Two of them at once.
+__device__ __forceinline__ bool barrier_wait_both(uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1, volatile int *stop)
+{
+    const bool first = barrier_try(bar0, parity0), second = barrier_try(bar1, parity1);
+    if (__all_sync(0xFFFFFFFFu, first && second))
+        return true;
+    return barrier_wait_warp(bar0, parity0, stop) && barrier_wait_warp(bar1, parity1, stop);
+}
+
 // After a wait that gave up: long enough for every copy and product in flight to end.
 __device__ __forceinline__ void let_copies_land()
 {
@@ -138,6 +147,11 @@ __device__ __forceinline__ void copy_async_arrive(uint32_t bar)
 __device__ __forceinline__ void copy_async_wait()
 {
     asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+__device__ __forceinline__ void store_shared(uint32_t at, const uint4 &v)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
 // Shared memory written by this thread becomes visible to the tensor cores.
