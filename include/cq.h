@@ -270,6 +270,12 @@ cq_status cq_w4_linear_backward(const void *dz, int64_t lddz, const void *x, int
 cq_status cq_activation_backward(const void *dy, int64_t lddy, const void *pre, int64_t ldpre, int dtype, int64_t T,
                                  int64_t R, int activation, void *dz, int64_t lddz, float *dbias, void *stream);
 
+/* The layer's and its gradients' kernels hand work from warp to warp through bounded waits.  A wait that has not ended
+ * after four seconds gives up: the kernel then returns, its outputs unfinished.  This call synchronises `stream` and
+ * returns CQ_ERR_CUDA when that has happened on the current device since the library was loaded (or when the stream
+ * reports an error), else CQ_OK. */
+cq_status cq_w4_status(void *stream);
+
 /* Rows of a quantised table, from the selection's own scales [V*K/128] and codes [V*K/128][16] of a [V][K] matrix:
  * out[t][i] = multiplier * (scale * q) of row ids[t], each product in fp32, rounded once to dtype (CQ_DTYPE_FP32 too);
  * an id outside [0, V) gives a row of zeros.  ids are int32 (ids64 == 0) or int64 (ids64 == 1), out is [T][K]

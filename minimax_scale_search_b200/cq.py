@@ -29,7 +29,7 @@ MAX_E = 8
 EXPORTS = ("cq_workspace_bytes", "cq_select_scales", "cq_select_scales_ex", "cq_select_scales_host",
            "cq_absmax_scales", "cq_pool_diagonals", "cq_group_objective", "cq_reconstruction_proxy",
            "cq_gptq_export", "cq_gptq_dequantize", "cq_w4_linear", "cq_w4_linear_backward",
-           "cq_activation_backward", "cq_w4_embedding", "cq_w4_embedding_backward_workspace_bytes",
+           "cq_activation_backward", "cq_w4_status", "cq_w4_embedding", "cq_w4_embedding_backward_workspace_bytes",
            "cq_w4_embedding_backward", "cq_estimate_diagonals", "cq_select_scales_spec",
            "cq_select_scales_noalloc", "cq_trim_memory", "cq_read_counters", "cq_get_status", "cq_status_string",
            "cq_version")
@@ -88,6 +88,8 @@ def _load():
     L.cq_w4_linear_backward.argtypes = [vp, i64, vp, i64, i32, i64, vp, vp, vp, i64, i64, vp, i64, vp, vp]
     L.cq_activation_backward.restype = i32
     L.cq_activation_backward.argtypes = [vp, i64, vp, i64, i32, i64, i64, i32, vp, i64, vp, vp]
+    L.cq_w4_status.restype = i32
+    L.cq_w4_status.argtypes = [vp]
     L.cq_w4_embedding.restype = i32
     L.cq_w4_embedding.argtypes = [vp, i32, i64, vp, vp, i64, i64, ctypes.c_float, i32, vp, vp]
     L.cq_w4_embedding_backward_workspace_bytes.restype = ctypes.c_size_t
@@ -726,6 +728,14 @@ def activation_backward(dy, pre, activation: str, *, want_dbias: bool = True, st
     _call(context, lib.cq_activation_backward, dy.data_ptr(), lddy, pre.data_ptr(), ldpre, dt, T, R, act, out.data_ptr(),
           lddz, None if dbias is None else dbias.data_ptr(), handle)
     return out, dbias
+
+
+def w4_status(stream=None) -> int:
+    """Synchronises ``stream`` and returns CQ_OK; raises CQError when a wait inside a
+    kernel of w4_linear or w4_linear_backward has given up on the current device
+    (its outputs are then unfinished)."""
+    _check(lib.cq_w4_status(_stream_handle(stream)), "cq_w4_status")
+    return CQ_OK
 
 
 def _table(ids, codes, K):

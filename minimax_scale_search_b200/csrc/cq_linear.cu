@@ -1195,4 +1195,14 @@ cq_status cq_activation_backward(const void *dy, int64_t lddy, const void *pre, 
     return launched();
 }
 
+cq_status cq_w4_status(void *stream)
+{
+    if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return CQ_ERR_CUDA;
+    int gave_up = 0;
+    if (cudaMemcpyFromSymbol(&gave_up, g_gave_up, sizeof(gave_up)) != cudaSuccess)
+        return CQ_ERR_CUDA;
+    return gave_up ? CQ_ERR_CUDA : CQ_OK;
+}
+
 }  // extern "C"

@@ -459,3 +459,77 @@ def test_a_side_stream():
     ds = cq.w4_linear_backward(y, late, w, stream=s)[1]
     s.synchronize()
     assert torch.equal(y, ref) and torch.equal(ds, ref_ds)
+
+
+def test_offsets_beyond_32_bits():
+    """Outputs of more than 2^31 elements: the rows at and behind the border against a small call of the same rows."""
+    import torch
+    from minimax_scale_search_b200 import cq
+    T, R, K = 70001, 32768, 128
+    w, _, _ = make_layer(R, K, 21)
+    x = torch.randn((T, K), device="cuda").half()
+    rows = torch.tensor([0, 1, 65535, 65536, 65537, *range(T - 60, T)], device="cuda")
+    y, pre = cq.w4_linear(x, w, activation="silu", want_pre=True)
+    y2, pre2 = cq.w4_linear(x[rows], w, activation="silu", want_pre=True)
+    assert torch.equal(y[rows], y2) and torch.equal(pre[rows], pre2)
+    dz, db = cq.activation_backward(y, pre, "silu", out=y)  # in place
+    dz2, _ = cq.activation_backward(y2, pre2, "silu")
+    assert torch.equal(dz[rows], dz2) and torch.isfinite(db).all()
+    del pre
+    dx, ds = cq.w4_linear_backward(dz, x, w)
+    dx2, _ = cq.w4_linear_backward(dz2, None, w, want_dscales=False)
+    # the small call shares the contraction of R among CTAs: each side's sum is off by at most R 2^-23 of its terms' sum
+    terms = (dz2.double().abs() @ torch.from_numpy(np.abs(w4.weight(*make_layer(R, K, 21)[1:]))).cuda())
+    assert bool(((dx[rows].double() - dx2.double()).abs() <= terms * 2 * (R * 2.0 ** -23) + 2 * U["fp16"] * dx2.double().abs() + TINY["fp16"]).all())
+    half = 35008
+    parts = sum(cq.w4_linear_backward(d, v, w, want_dx=False)[1].double() for d, v in ((dz[:half], x[:half]), (dz[half:], x[half:])))
+    assert bool(((ds.double() - parts).norm() <= 1e-5 * parts.norm()))  # 136 spans of 512 tokens added in fp32, each 2^-24 off
+    assert cq.w4_status() == cq.CQ_OK
+
+
+def test_table_offsets_beyond_32_bits():
+    import torch
+    from minimax_scale_search_b200 import cq
+    T, V, K = 20001, 64, 131072
+    scales, codes = (device(a) for a in synth.make_codes(V * K // 128, seed=9))
+    scales = torch.full_like(scales, 0x2000)
+    ids = torch.randint(-1, V + 1, (T,), device="cuda")
+    out = cq.w4_embedding(ids, scales, codes, K)
+    rows = torch.tensor([0, 16383, 16384, 16385, *range(T - 5, T)], device="cuda")
+    assert torch.equal(out[rows], cq.w4_embedding(ids[rows], scales, codes, K))
+    g = cq.w4_embedding_backward(out, ids, codes)
+    few = cq.w4_embedding_backward(out[-300:].contiguous(), ids[-300:].contiguous(), codes)
+    count = torch.bincount(ids[(ids >= 0) & (ids < V)], minlength=V)
+    late = torch.bincount(ids[-300:][(ids[-300:] >= 0) & (ids[-300:] < V)], minlength=V)
+    # every token of a row has the same dots: a row's sum is its count of them (fp64 sums, rounded once)
+    expect = few.double() / late.clamp(min=1)[:, None] * count[:, None]
+    named = late > 0
+    assert bool(((g.double() - expect)[named].abs() <= 3 * 2.0 ** -24 * expect[named].abs()).all())
+
+
+def test_concurrent_calls_on_two_streams():
+    """No state is shared between calls: two streams with calls of every kind at once."""
+    import torch
+    from minimax_scale_search_b200 import cq
+    w, _, _ = make_layer(1032, 1152, 5)
+    scales, codes, _, _ = make_table(500, 1152, 5)
+    work = []
+    for T in (9, 700):
+        x, _ = values(np.random.default_rng(T), (T, 1152), "bf16")
+        dz, _ = values(np.random.default_rng(T + 1), (T, 1032), "bf16")
+        work.append((x, dz, torch.randint(-1, 500, (T,), device="cuda")))
+
+    def all_of(x, dz, ids, stream):
+        return (cq.w4_linear(x, w, stream=stream), *cq.w4_linear_backward(dz, x, w, stream=stream),
+                *cq.activation_backward(dz, dz, "gelu", stream=stream),
+                cq.w4_embedding(ids, scales, codes, 1152, stream=stream),
+                cq.w4_embedding_backward(x, ids, codes, stream=stream))
+
+    refs = [all_of(*v, None) for v in work]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[all_of(*v, s) for v, s in zip(work, streams)] for _ in range(20)]
+    torch.cuda.synchronize()
+    for run in got:
+        for a, b in zip(run, refs):
+            assert all(torch.equal(i, j) for i, j in zip(a, b))
