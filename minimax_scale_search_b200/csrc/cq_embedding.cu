@@ -11,7 +11,7 @@
 //  1. dots[t][g] = sum_{i in g} dout[t][i] q[id_t][i] (fp32, one pass over dout, which is what
 //     bounds the whole); the same launch fills dscales with zeros and sorts the tokens by
 //     (id, t): up to kRankMost tokens by counting, for each, the tokens before it (T^2
-//     comparisons, no further launch), above with a radix sort of its own launches;
+//     comparisons, no further launch), others with a radix sort of its own launches;
 //  2. sums over the runs of equal ids within each chunk of 8 sorted tokens, in fp64; a run that
 //     lies inside a chunk is done, others leave a part at the chunk's head or tail;
 //  3. the runs across chunks, from their parts in order.
@@ -25,9 +25,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kUnits = kThreads / kWordsPerGroup;       // units of a CTA at a time: kGroups groups of one token
-constexpr int kRankMost = 8192;                         // tokens sorted by counting
+constexpr int kRankMost = 8192;                         // tokens sorted by counting,
+constexpr int64_t kRankRows = 1 << 24;                  // of tables whose row numbers fp32 holds
 constexpr int kRankBlock = 32;                          // tokens ranked by a CTA, one a lane
-constexpr int kRankTile = kRankMost;                    // keys in shared memory at a time: all (tiles of 1024 were slower, 28 us for 18)
 constexpr int kChunk = 8;                               // sorted tokens per partial sum
 constexpr int kSortTokens = 1024;                       // per CTA of the radix sort
 
@@ -163,44 +163,50 @@ __global__ void __launch_bounds__(kThreads) embedding_kernel(Ids ids, int64_t T,
 // ---- gradient ------------------------------------------------------------------------------------
 
 // order[rank] = t, key[rank] = row: for each of a CTA's 32 tokens, one a lane, the number of tokens before it
-// by (row, t).  The warps take an eighth of the tokens each to compare with, four per shared read.
-// (128 tokens per CTA, four a lane, had fewer reads and took twice as long: too few CTAs.)
+// by (row, t).  The warps take an eighth of the tokens each to compare with, four per shared read.  A comparison of
+// row numbers is the difference clamped to [0, 1], in fp32, where it and its sum are one instruction each.
 __device__ void rank_tokens(const Ids &ids, int T, int t0, uint32_t *key, int32_t *order)
 {
     constexpr int kWarps = kThreads / 32;
-    __shared__ alignas(16) uint32_t tile[kRankTile];
+    __shared__ alignas(16) float tile[kRankMost];
     __shared__ int ranks[kWarps][kRankBlock];
+    static_assert(kRankMost % kThreads == 0 && kThreads % (32 * kWarps) == 0 && kRankBlock == 32, "shares are blocks of 32");
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, t = t0 + lane;
-    const uint32_t mine = t < T ? ids.key(t) : 0;
-    int rank = 0;
-    static_assert(kRankTile % kThreads == 0 && kThreads % (32 * kWarps) == 0 && kRankBlock == 32, "shares are blocks of 32");
-    const int end = (T + kThreads - 1) / kThreads * kThreads;  // the keys that are there, and some that are above all
+    const uint32_t row = t < T ? ids.key(t) : 0;
+    const float mine = static_cast<float>(row);
+    const int end = (T + kThreads - 1) / kThreads * kThreads;  // the tokens that are there, and some that are above all
 #pragma unroll 8
     for (int j = threadIdx.x; j < end; j += kThreads)
-        tile[j] = j < T ? ids.key(j) : 0xFFFFFFFFu;
+        tile[j] = j < T ? static_cast<float>(ids.key(j)) : 2.0f * kRankRows;
     __syncthreads();
     // (other, j) < (mine, t)  <=>  other < mine + (j < t)
+    float rank[4] = {};
     const int share = end / kWarps;  // % 32 == 0
     for (int j0 = warp * share; j0 < (warp + 1) * share; j0 += 32) {
         if (j0 != t0) {
-            const uint32_t below = mine + (j0 < t0);
-            const uint4 *p = reinterpret_cast<const uint4 *>(tile + j0);
+            const float below = mine + (j0 < t0 ? 1.0f : 0.0f);
+            const float4 *p = reinterpret_cast<const float4 *>(tile + j0);
 #pragma unroll
-            for (int j = 0; j < 8; j++)
-                rank += (p[j].x < below) + (p[j].y < below) + (p[j].z < below) + (p[j].w < below);
+            for (int j = 0; j < 8; j++) {
+                const float4 o = p[j];
+                rank[0] += __saturatef(below - o.x);
+                rank[1] += __saturatef(below - o.y);
+                rank[2] += __saturatef(below - o.z);
+                rank[3] += __saturatef(below - o.w);
+            }
         } else {
             for (int j = j0; j < j0 + 32; j++)
-                rank += tile[j] < mine + (j < t);
+                rank[0] += __saturatef(mine + (j < t ? 1.0f : 0.0f) - tile[j]);
         }
     }
-    ranks[warp][lane] = rank;
+    ranks[warp][lane] = static_cast<int>(rank[0] + rank[1] + rank[2] + rank[3]);
     __syncthreads();
     if (warp == 0 && t < T) {
         int r = 0;
 #pragma unroll
         for (int i = 0; i < kWarps; i++)
             r += ranks[i][lane];
-        key[r] = mine;
+        key[r] = row;
         order[r] = t;
     }
 }
@@ -543,7 +549,6 @@ struct Workspace {
     Workspace(int64_t T, int64_t K)
     {
         const size_t n = static_cast<size_t>(T), ng = static_cast<size_t>(K / kGroup), chunks = (n + kChunk - 1) / kChunk;
-        const size_t sorted = T > kRankMost ? n * 4 : 0;
         size_t at = 0;
         auto take = [&](size_t size) {
             const size_t here = at;
@@ -552,9 +557,9 @@ struct Workspace {
         };
         key = take(n * 4);
         order = take(n * 4);
-        key2 = take(sorted);
-        order2 = take(sorted);
-        counts = take(T > kRankMost ? (n + kSortTokens - 1) / kSortTokens * 256 * 4 : 0);
+        key2 = take(n * 4);
+        order2 = take(n * 4);
+        counts = take((n + kSortTokens - 1) / kSortTokens * 256 * 4);
         dots = take(n * ng * 4);
         head = take(chunks * ng * 8);
         tail = take(chunks * ng * 8);
@@ -651,8 +656,9 @@ cq_status cq_w4_embedding_backward(const void *dout, int dtype, const void *ids,
     const Parts parts = {reinterpret_cast<double *>(base + ws.head), reinterpret_cast<double *>(base + ws.tail)};
     const Ids in = {ids, ids64, V};
 
-    const int rank_blocks = T <= kRankMost ? static_cast<int>((T + kRankBlock - 1) / kRankBlock) : 0;
-    if (T > kRankMost && sort_tokens(in, T, base, ws, s) != CQ_OK)
+    const bool count = T <= kRankMost && V < kRankRows;
+    const int rank_blocks = count ? static_cast<int>((T + kRankBlock - 1) / kRankBlock) : 0;
+    if (!count && sort_tokens(in, T, base, ws, s) != CQ_OK)
         return CQ_ERR_CUDA;
     const cq_status made = by_groups(ng, [&](auto groups) {
         constexpr int kGroups = decltype(groups)::value;

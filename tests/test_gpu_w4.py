@@ -310,6 +310,24 @@ def test_embedding_gradient_of_every_order_of_tokens(T, kind):
     assert np.all(np.abs(f64(g)[:, 0] - e) <= A * (128 + 2) * 2.0 ** -24)
 
 
+@pytest.mark.parametrize("T", [5, 700])
+def test_a_table_of_more_rows_than_fp32_counts(T):
+    """2^24 + 3 rows: neighbouring row numbers that fp32 does not tell apart stay apart."""
+    import torch
+    from minimax_scale_search_b200 import cq
+    V, K = (1 << 24) + 3, 128
+    codes = torch.randint(-2 ** 31, 2 ** 31 - 1, (V, 16), dtype=torch.int32, device="cuda")
+    ids = V - 1 - torch.arange(T, device="cuda") % 4
+    d = torch.randn((T, K), device="cuda")
+    g = cq.w4_embedding_backward(d, ids, codes)
+    few = codes[V - 4:].cpu().numpy().view(np.uint32)
+    q = w4.table(np.ones(4, np.uint16), few, K)[0]
+    e = w4.embedding_backward(f64(d), (ids - (V - 4)).cpu().numpy(), q)
+    A = w4.embedding_backward(np.abs(f64(d)), (ids - (V - 4)).cpu().numpy(), np.abs(q))
+    assert np.all(np.abs(f64(g[V - 4:]) - e) <= A * (128 + 2) * 2.0 ** -24)
+    assert int((g != 0).sum()) <= 4
+
+
 def test_ids_of_any_shape_and_a_shared_workspace():
     import torch
     from minimax_scale_search_b200 import cq
