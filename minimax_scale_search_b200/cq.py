@@ -650,6 +650,8 @@ def w4_linear(x, w: W4Weights, *, bias=None, activation: str = "none", residual=
         ldy = _rows16("out", out, T, R, x)
         if _overlap(out, x):
             raise ValueError("out must not overlap x")
+        if residual is not None and _overlap(out, residual) and (out.data_ptr() != residual.data_ptr() or ldy != ldres):
+            raise ValueError("out must be the residual itself, or not overlap it")
     ldpre = 0
     if want_pre:
         if pre is None:

@@ -235,6 +235,37 @@ def test_empty_calls():
     assert not g.any()
 
 
+def test_a_layer_without_outputs():
+    import torch
+    from minimax_scale_search_b200 import cq
+    z = lambda *shape, dtype=torch.int32: torch.zeros(shape, dtype=dtype, device="cuda")  # noqa: E731
+    w = cq.w4_weights(cq.GPTQTensors(z(32, 0), z(2, 0), z(2, 0, dtype=torch.float16), torch.arange(256, dtype=torch.int32, device="cuda") // 128))
+    x = torch.ones((5, 256), dtype=torch.bfloat16, device="cuda")
+    assert cq.w4_linear(x, w).shape == (5, 0)
+    dx, ds = cq.w4_linear_backward(x[:, :0], x, w, dx=torch.ones_like(x))
+    assert not dx.any() and ds.shape == (2, 0)
+
+
+def test_operands_that_overlap_are_refused():
+    import torch
+    from minimax_scale_search_b200 import cq
+    w, _, _ = make_layer(256, 256, 1)
+    buf = torch.zeros((20, 256), dtype=torch.float16, device="cuda")
+    x = torch.zeros((8, 256), dtype=torch.float16, device="cuda")
+    with pytest.raises(ValueError, match="overlap x"):
+        cq.w4_linear(buf[:8], w, out=buf[4:12])
+    with pytest.raises(ValueError, match="residual itself"):
+        cq.w4_linear(x, w, residual=buf[:8], out=buf[1:9])
+    with pytest.raises(ValueError, match="pre must not overlap"):
+        cq.w4_linear(x, w, out=buf[:8], want_pre=True, pre=buf[7:15])
+    with pytest.raises(ValueError, match="only with want_pre"):
+        cq.w4_linear(x, w, pre=buf[:8])
+    with pytest.raises(ValueError, match="dx must not overlap"):
+        cq.w4_linear_backward(buf[:8], x, w, dx=buf[2:10])
+    with pytest.raises(ValueError, match="dy or pre itself"):
+        cq.activation_backward(buf[:8], x, "silu", out=buf[1:9])
+
+
 def test_act_order_is_refused():
     import torch
     from minimax_scale_search_b200 import cq
