@@ -10,8 +10,9 @@ line with the device time per call (CUDA events), groups/s and the kernel
 counters; with --qmin/--qmax/--group-size it runs the general-spec path
 instead.  --ops runs each of the other kernels once (AbsMax, objective of
 given scales, GPTQ export and dequantisation, diagonal estimation, the
-three-policy reconstruction proxy) on inputs larger than L2 and prints their
-device times.
+three-policy reconstruction proxy, the linear layer and the table lookup on the
+exported weights with their gradients) on inputs larger than L2 and prints
+their device times.
 """
 from __future__ import annotations
 
@@ -30,6 +31,29 @@ def timed(fn):
     e1.record()
     torch.cuda.synchronize()
     return out, round(e0.elapsed_time(e1), 3)
+
+
+def run_layer_ops(scales, codes, t, X, ms):
+    """The operators on 4-bit weights, on the exported 4,096 x 16,384 layer: one new
+    token, 4,096 tokens forwards and backwards, and the layer's rows as a table."""
+    import torch
+
+    from minimax_scale_search_b200 import cq
+    w = cq.w4_weights(t)
+    x = X[:4096]
+    ids = torch.arange(8192, device="cuda") * 37 % 4096
+    for name, fn in (("linear_1_token", lambda: cq.w4_linear(x[:1], w)),
+                     ("linear_4096_tokens", lambda: cq.w4_linear(x, w, activation="silu", want_pre=True)),
+                     ("activation_backward", lambda: cq.activation_backward(y, pre, "silu")),
+                     ("linear_backward", lambda: cq.w4_linear_backward(y, x, w)),
+                     ("embedding", lambda: cq.w4_embedding(ids, scales, codes, 16384, dtype=torch.bfloat16)),
+                     ("embedding_backward", lambda: cq.w4_embedding_backward(e, ids, codes))):
+        fn()  # the first call loads the kernel
+        out, ms[name] = timed(fn)
+        if name == "linear_4096_tokens":
+            y, pre = out
+        elif name == "embedding":
+            e = out
 
 
 def run_ops():
@@ -53,6 +77,7 @@ def run_ops():
     g.manual_seed(5)
     X = torch.randn((4 * 8192, 16384), generator=g, device="cuda").to(torch.bfloat16)
     _, ms["diagonals"] = timed(lambda: cq.estimate_diagonals(X, np.arange(5, dtype=np.int64) * 8192))
+    run_layer_ops(s_abs, c_abs, t, X, ms)
     Wp, Dp, off = synth.make_proxy_inputs()
     res, ms["proxy_three_policies"] = timed(lambda: cq.evaluate_policies(
         torch.from_numpy(Wp.view(np.int16)).cuda(), torch.from_numpy(Dp).cuda(), off))
