@@ -500,11 +500,10 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
     cluster.sync();  // peers keep their shared memory until it has been read
 }
 
-
 // ---- few rows ----------------------------------------------------------------------------------
 //
 // Up to 16 rows the weights' bytes are the work.  A CTA has 128 outputs and a part of the groups (a
-// cluster has them all); one warp keeps a ring of groups in flight (words by tensor map, scales, zero
+// cluster has them all); two warps keep a ring of groups in flight (words by tensor map; scales, zero
 // points and the tokens' 128 inputs by asynchronous copies), eight warps in four sets take them in turn,
 // 64 outputs a warp.  A thread reads 4 adjacent outputs' words at once; a word is 8 inputs, whose pairs
 // (q, q + 4) come out of it with a shift and a mask.  That order of the inputs is as good as any for the
