@@ -87,6 +87,25 @@ __device__ __forceinline__ float half_bits(uint16_t b)
     return __half2float(__ushort_as_half(b));
 }
 
+// Phi(z), the normal distribution function, and phi(z), its density: the tail beyond |z| is phi M(|z|), M the ratio of
+// Mills, here a polynomial of degree 8 in 1 / (1 + 0.3 |z|) (fitted for the least largest relative error on [0, 14], 1.3e-7), so that the
+// small values of large negative z keep their digits.  17 instructions, where erfc has three times as many.
+__device__ __forceinline__ float normal_distribution(float z, float &phi)
+{
+    const float t = __fdividef(1.0f, fmaf(0.3f, fabsf(z), 1.0f));
+    float m = 0.08939834282074922f;
+    m = fmaf(m, t, -0.3938665763259987f);
+    m = fmaf(m, t, 0.5167975709357504f);
+    m = fmaf(m, t, -0.13402152701818226f);
+    m = fmaf(m, t, 0.3219068215590072f);
+    m = fmaf(m, t, 0.2505677419384999f);
+    m = fmaf(m, t, 0.30266395988252076f);
+    m = fmaf(m, t, 0.2998676368875933f);
+    phi = 0.3989422804014327f * __expf(-0.5f * z * z);
+    const float tail = phi * (m * t);
+    return z < 0.0f ? tail : 1.0f - tail;
+}
+
 // act(z) for a result that is rounded to 16 bits: exp and the quotient to a few units of
 // 2^-22, far inside that rounding.  The quotients' limits hold: exp(-z) = inf gives 0.
 template <int n>
@@ -96,10 +115,12 @@ __device__ __forceinline__ void activate(float (&z)[n], int act)
 #pragma unroll
         for (int i = 0; i < n; i++)
             z[i] = z[i] < 0.0f ? 0.0f : z[i];
-    } else if (act == CQ_ACT_GELU) {  // erfc keeps the small values of large negative z
+    } else if (act == CQ_ACT_GELU) {
 #pragma unroll
-        for (int i = 0; i < n; i++)
-            z[i] = 0.5f * z[i] * erfcf(z[i] * -0.7071067811865476f);
+        for (int i = 0; i < n; i++) {
+            float phi;
+            z[i] *= normal_distribution(z[i], phi);
+        }
     } else if (act == CQ_ACT_GELU_TANH) {  // z/2 (1 + tanh u) = z / (1 + exp(-2u))
 #pragma unroll
         for (int i = 0; i < n; i++)
@@ -122,8 +143,11 @@ __device__ __forceinline__ void slopes(float (&z)[n], int act)
             z[i] = z[i] > 0.0f ? 1.0f : 0.0f;
     } else if (act == CQ_ACT_GELU) {
 #pragma unroll
-        for (int i = 0; i < n; i++)
-            z[i] = 0.5f * erfcf(z[i] * -0.7071067811865476f) + z[i] * (0.3989422804014327f * __expf(-0.5f * z[i] * z[i]));
+        for (int i = 0; i < n; i++) {
+            float phi;
+            const float p = normal_distribution(z[i], phi);
+            z[i] = fmaf(z[i], phi, p);
+        }
     } else if (act == CQ_ACT_GELU_TANH) {  // p = (1 + tanh u) / 2 = 1 / (1 + exp(-2u)), 1 - tanh^2 u = 4 p (1 - p)
 #pragma unroll
         for (int i = 0; i < n; i++) {
