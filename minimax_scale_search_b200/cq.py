@@ -563,12 +563,12 @@ def _place(dev, stream):
     return stream.cuda_stream, torch.cuda.stream(stream)
 
 
-def _empty(context, shape, dtype, dev):
-    import torch
+def _empty(context, shape, like, dtype=None):
+    """An uninitialised tensor on the device of `like`, of its type where none is given."""
     if context is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape, dtype=dtype) if dtype is not None else like.new_empty(shape)
     with context:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape, dtype=dtype or like.dtype)
 
 
 def _call(context, function, *args):
@@ -597,13 +597,23 @@ def _rows16(name, t, rows, cols, like):
     return ld
 
 
+_codes = {}  # torch dtype: CQ_DTYPE_*, filled at first use
+
+
+def _float_code(dtype):
+    if not _codes:
+        import torch
+        _codes.update({torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_FP16, torch.float32: DTYPE_FP32})
+    return _codes.get(dtype)
+
+
 def _dtype16(name, t):
-    import torch
     if not t.is_cuda or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D CUDA tensor")
-    if t.dtype not in (torch.bfloat16, torch.float16):
+    code = _float_code(t.dtype)
+    if code is None or code == DTYPE_FP32:
         raise ValueError(f"{name} must be bfloat16 or float16")
-    return DTYPE_BF16 if t.dtype == torch.bfloat16 else DTYPE_FP16
+    return code
 
 
 def _activation(activation):
@@ -645,7 +655,7 @@ def w4_linear(x, w: W4Weights, *, bias=None, activation: str = "none", residual=
     ldres = _rows16("residual", residual, T, R, x) if residual is not None else 0
     handle, context = _place(x.device, stream)
     if out is None:
-        out, ldy = _empty(context, (T, R), x.dtype, x.device), R
+        out, ldy = _empty(context, (T, R), x), R
     else:
         ldy = _rows16("out", out, T, R, x)
         if _overlap(out, x):
@@ -655,7 +665,7 @@ def w4_linear(x, w: W4Weights, *, bias=None, activation: str = "none", residual=
     ldpre = 0
     if want_pre:
         if pre is None:
-            pre, ldpre = _empty(context, (T, R), x.dtype, x.device), R
+            pre, ldpre = _empty(context, (T, R), x), R
         else:
             ldpre = _rows16("pre", pre, T, R, x)
             if _overlap(pre, x) or _overlap(pre, out) or (residual is not None and _overlap(pre, residual)):
@@ -683,7 +693,7 @@ def w4_linear_backward(dz, x, w: W4Weights, *, want_dx: bool = True, want_dscale
     if not want_dx:
         dx = None
     elif dx is None:
-        dx, lddx = _empty(context, (T, K), dz.dtype, dz.device), K
+        dx, lddx = _empty(context, (T, K), dz), K
     else:
         lddx = _rows16("dx", dx, T, K, dz)
         if _overlap(dx, dz) or (want_dscales and _overlap(dx, x)):
@@ -693,7 +703,7 @@ def w4_linear_backward(dz, x, w: W4Weights, *, want_dx: bool = True, want_dscale
     else:
         ldx = _rows16("x", x, T, K, dz)
         if dscales is None:
-            dscales = _empty(context, (K // GROUP, R), torch.float32, dz.device)
+            dscales = _empty(context, (K // GROUP, R), dz, torch.float32)
         elif (dscales.shape != (K // GROUP, R) or dscales.dtype != torch.float32 or dscales.device != dz.device or
               not dscales.is_contiguous() or dscales.data_ptr() % 16):
             raise ValueError(f"dscales must be contiguous 16-byte aligned float32 [{K // GROUP}, {R}]")
@@ -715,7 +725,7 @@ def activation_backward(dy, pre, activation: str, *, want_dbias: bool = True, st
     lddy, ldpre = _rows16("dy", dy, T, R, dy), _rows16("pre", pre, T, R, dy)
     handle, context = _place(dy.device, stream)
     if out is None:
-        out, lddz = _empty(context, (T, R), dy.dtype, dy.device), R
+        out, lddz = _empty(context, (T, R), dy), R
     else:
         lddz = _rows16("out", out, T, R, dy)
         for t, ld in ((dy, lddy), (pre, ldpre)):
@@ -724,7 +734,7 @@ def activation_backward(dy, pre, activation: str, *, want_dbias: bool = True, st
     if not want_dbias:
         dbias = None
     elif dbias is None:
-        dbias = _empty(context, (R,), torch.float32, dy.device)
+        dbias = _empty(context, (R,), dy, torch.float32)
     elif dbias.shape != (R,) or dbias.dtype != torch.float32 or dbias.device != dy.device or not dbias.is_contiguous():
         raise ValueError(f"dbias must be contiguous float32 [{R}]")
     _call(context, lib.cq_activation_backward, dy.data_ptr(), lddy, pre.data_ptr(), ldpre, dt, T, R, act, out.data_ptr(),
@@ -753,14 +763,10 @@ def _table(ids, codes, K):
 
 
 def _float_type(name, dtype):
-    import torch
-    if dtype is torch.bfloat16:
-        return DTYPE_BF16
-    if dtype is torch.float16:
-        return DTYPE_FP16
-    if dtype is torch.float32:
-        return DTYPE_FP32
-    raise ValueError(f"{name} must be bfloat16, float16 or float32")
+    code = _float_code(dtype)
+    if code is None:
+        raise ValueError(f"{name} must be bfloat16, float16 or float32")
+    return code
 
 
 def w4_embedding(ids, scales, codes, K: int, *, multiplier: float = 1.0, dtype=None, stream=None, out=None):
@@ -780,7 +786,7 @@ def w4_embedding(ids, scales, codes, K: int, *, multiplier: float = 1.0, dtype=N
     shape = (*ids.shape, K)
     handle, context = _place(ids.device, stream)
     if out is None:
-        out = _empty(context, shape, dtype, ids.device)
+        out = _empty(context, shape, ids, dtype)
     elif out.shape != shape or out.dtype != dtype or out.device != ids.device or not out.is_contiguous():
         raise ValueError(f"out must be contiguous {dtype} {list(shape)}")
     _call(context, lib.cq_w4_embedding, ids.data_ptr(), int(ids.dtype is torch.int64), T, scales.data_ptr(), codes.data_ptr(),
@@ -812,11 +818,11 @@ def w4_embedding_backward(dout, ids, codes, *, multiplier: float = 1.0, stream=N
         raise ValueError(f"workspace must hold {wsb} contiguous bytes on the device of ids")
     handle, context = _place(ids.device, stream)
     if out is None:
-        out = _empty(context, (V, K // GROUP), torch.float32, ids.device)
+        out = _empty(context, (V, K // GROUP), ids, torch.float32)
     elif out.shape != (V, K // GROUP) or out.dtype != torch.float32 or out.device != ids.device or not out.is_contiguous():
         raise ValueError(f"out must be contiguous float32 [{V}, {K // GROUP}]")
     if workspace is None:
-        workspace = _empty(context, (wsb,), torch.uint8, ids.device)
+        workspace = _empty(context, (wsb,), ids, torch.uint8)
     _call(context, lib.cq_w4_embedding_backward, dout.data_ptr(), dt, ids.data_ptr(), int(ids.dtype is torch.int64), T,
           codes.data_ptr(), V, K, multiplier, out.data_ptr(), workspace.data_ptr(), wsb, handle)
     return out

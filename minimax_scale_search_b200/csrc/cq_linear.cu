@@ -1032,7 +1032,7 @@ cq_status launch_clusters(void (*kernel)(P...), int64_t ctas, int ranks, int thr
     attr[0].val.clusterDim.x = static_cast<unsigned>(ranks);
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     config.attrs = attr;
-    config.numAttrs = 1;
+    config.numAttrs = ranks > 1 ? 1 : 0;
     return cudaLaunchKernelEx(&config, kernel, std::forward<A>(args)...) == cudaSuccess ? CQ_OK : CQ_ERR_CUDA;
 }
 
