@@ -259,7 +259,7 @@ cq_status cq_w4_linear(const void *x, int64_t ldx, int dtype, int64_t T, const i
  *  dscales  fp32 [K/128][R], nullable: dscales[g][r] = sum_{i in g} (u - z - 1)[r][i] sum_t dz[t][r] x[t][i];
  *           written, not added to.  x is read only for it (nullable otherwise).
  * The gradient of the residual is the gradient of y itself; that of the bias comes from
- * cq_activation_backward.  Outputs must not overlap inputs. */
+ * cq_activation_backward.  Outputs must not overlap inputs or each other (they may be written at the same time). */
 cq_status cq_w4_linear_backward(const void *dz, int64_t lddz, const void *x, int64_t ldx, int dtype, int64_t T,
                                 const int32_t *qweight, const int32_t *qzeros, const uint16_t *gptq_scales, int64_t R,
                                 int64_t K, void *dx, int64_t lddx, float *dscales, void *stream);
@@ -287,7 +287,8 @@ cq_status cq_w4_embedding(const void *ids, int ids64, int64_t T, const uint16_t 
  *   dscales[v][g] = multiplier * sum_{t: ids[t] = v} sum_{i in g} dout[t][i] q[v][i]    fp32 [V][K/128]
  * written whole (zero for a row that no id names).  The tokens are sorted by id (stable), the sums over a
  * row's tokens taken in fp64 in a fixed order.  workspace: device, 256-byte aligned, at least
- * cq_w4_embedding_backward_workspace_bytes(T, K); calls that share one must be ordered on one stream. T < 2^31. */
+ * cq_w4_embedding_backward_workspace_bytes(T, K); calls that share one must be ordered on one stream. T < 2^31.
+ * dscales and workspace must not overlap an input or each other. */
 size_t cq_w4_embedding_backward_workspace_bytes(int64_t T, int64_t K);
 cq_status cq_w4_embedding_backward(const void *dout, int dtype, const void *ids, int ids64, int64_t T,
                                    const uint32_t *codes, int64_t V, int64_t K, float multiplier, float *dscales,

@@ -244,6 +244,7 @@ __global__ void __launch_bounds__(kThreads) dots_kernel(const void *__restrict__
                                                         float *__restrict__ dots, int rank_blocks, uint32_t *key, int32_t *order,
                                                         float *__restrict__ dscales)
 {
+    let_next_begin();
     if (static_cast<int>(blockIdx.x) < rank_blocks) {
         rank_tokens(ids, static_cast<int>(T), blockIdx.x * kRankBlock, key, order);
         return;
@@ -300,11 +301,14 @@ struct Parts {
     double *head, *tail;
 };
 
-// `width` threads (a power of two) have a chunk's groups.
-__global__ void __launch_bounds__(kThreads) chunk_sums_kernel(const uint32_t *__restrict__ key, const int32_t *__restrict__ order,
-                                                              int64_t T, int64_t V, const float *__restrict__ dots, int64_t ng,
-                                                              int width, float multiplier, Parts parts, float *__restrict__ dscales)
+// `width` threads (a power of two) have a chunk's groups.  No __restrict__ on what the launch before wrote: loads
+// through it might be moved ahead of the wait.
+__global__ void __launch_bounds__(kThreads) chunk_sums_kernel(const uint32_t *key, const int32_t *order, int64_t T, int64_t V,
+                                                              const float *dots, int64_t ng, int width, float multiplier,
+                                                              Parts parts, float *dscales)
 {
+    let_next_begin();
+    wait_for_previous();
     const int64_t c = static_cast<int64_t>(blockIdx.x) * (kThreads / width) + threadIdx.x / width;
     const int64_t p0 = c * kChunk, p1 = p0 + kChunk < T ? p0 + kChunk : T;
     if (p0 >= T)
@@ -351,9 +355,10 @@ __global__ void __launch_bounds__(kThreads) chunk_sums_kernel(const uint32_t *__
 
 // Runs that begin in chunk c and go on after it, a warp for each: `width` lanes (a power of two) have
 // a group each, 32 / width of them share its parts.
-__global__ void __launch_bounds__(kThreads) join_runs_kernel(const uint32_t *__restrict__ key, int64_t T, int64_t V, int64_t ng,
-                                                             int width, float multiplier, Parts parts, float *__restrict__ dscales)
+__global__ void __launch_bounds__(kThreads) join_runs_kernel(const uint32_t *key, int64_t T, int64_t V, int64_t ng, int width,
+                                                             float multiplier, Parts parts, float *dscales)
 {
+    wait_for_previous();
     const int lane = threadIdx.x % 32;
     const int64_t c = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32, p0 = c * kChunk;
     if (p0 + kChunk >= T)
@@ -680,13 +685,11 @@ cq_status cq_w4_embedding_backward(const void *dout, int dtype, const void *ids,
         width *= 2;
     const int64_t chunks = (T + kChunk - 1) / kChunk, per_block = kThreads / width;
     const unsigned grid = static_cast<unsigned>((chunks + per_block - 1) / per_block);
-    chunk_sums_kernel<<<grid, kThreads, 0, s>>>(key, order, T, V, dots, ng, width, multiplier, parts, dscales);
-    if (launched() != CQ_OK)
-        return CQ_ERR_CUDA;
-    if (chunks > 1)
-        join_runs_kernel<<<static_cast<unsigned>((chunks + kThreads / 32 - 1) / (kThreads / 32)), kThreads, 0, s>>>(
-            key, T, V, ng, width < 32 ? width : 32, multiplier, parts, dscales);
-    return launched();
+    const cq_status summed = launch_next(chunk_sums_kernel, grid, kThreads, 0, s, key, order, T, V, dots, ng, width, multiplier, parts, dscales);
+    if (summed != CQ_OK || chunks == 1)
+        return summed;
+    return launch_next(join_runs_kernel, static_cast<unsigned>((chunks + kThreads / 32 - 1) / (kThreads / 32)), kThreads, 0, s, key, T, V,
+                       ng, width < 32 ? width : 32, multiplier, parts, dscales);
 }
 
 }  // extern "C"

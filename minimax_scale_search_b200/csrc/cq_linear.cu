@@ -249,6 +249,8 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
     __syncthreads();
     tc::fence_after();
     const uint32_t tmem = tc::uniform(*tmem_at);
+    if (kGradient)
+        let_next_begin();  // the scale gradient's CTAs, as soon as SMs fall idle
 
     if (warp < 4) {
         // Epilogue, a warp's 32 m by 16 tokens at a time: a thread has one m in tensor memory;
@@ -937,6 +939,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     }
     if (warp == 5)
         tc::tmem_free(tmem, 2 * kGradN);
+    wait_for_previous();  // the input gradient before it: the two share inputs only
 }
 
 // dz = dy act'(pre) and its column sums.  A cluster of 8 CTAs owns 64 columns; its
@@ -1118,7 +1121,7 @@ cq_status layer(const uint16_t *x, int64_t ldx, int64_t T, const Layer &w, const
 
 template <class D>
 cq_status scale_gradient(const uint16_t *dz, int64_t lddz, const uint16_t *x, int64_t ldx, int64_t T, const Layer &w,
-                         float *dscales, cudaStream_t stream)
+                         float *dscales, bool after_dx, cudaStream_t stream)
 {
     if (T == 0)
         return cudaMemsetAsync(dscales, 0, static_cast<size_t>(w.K / kGroup) * w.R * 4, stream) == cudaSuccess ? CQ_OK : CQ_ERR_CUDA;
@@ -1130,7 +1133,10 @@ cq_status scale_gradient(const uint16_t *dz, int64_t lddz, const uint16_t *x, in
     if (allow_shared<kernel>(kGradBytes) != cudaSuccess)
         return CQ_ERR_CUDA;
     const int64_t tiles = (w.R + kM - 1) / kM * ((w.K + kGradN - 1) / kGradN), sms = sm_count();
-    kernel<<<static_cast<unsigned>(tiles < sms ? tiles : sms), kGradThreads, kGradBytes, stream>>>(dz_map, x_map, w, T, dscales);
+    const unsigned ctas = static_cast<unsigned>(tiles < sms ? tiles : sms);
+    if (after_dx)
+        return launch_next(kernel, ctas, kGradThreads, kGradBytes, stream, dz_map, x_map, w, T, dscales);
+    kernel<<<ctas, kGradThreads, kGradBytes, stream>>>(dz_map, x_map, w, T, dscales);
     return launched();
 }
 
@@ -1187,8 +1193,8 @@ cq_status cq_w4_linear_backward(const void *dz, int64_t lddz, const void *x, int
             return did;
     }
     if (dscales && R > 0)
-        return dtype == CQ_DTYPE_BF16 ? scale_gradient<BF16>(d, lddz, xs, ldx, T, w, dscales, s)
-                                      : scale_gradient<FP16>(d, lddz, xs, ldx, T, w, dscales, s);
+        return dtype == CQ_DTYPE_BF16 ? scale_gradient<BF16>(d, lddz, xs, ldx, T, w, dscales, dx != nullptr, s)
+                                      : scale_gradient<FP16>(d, lddz, xs, ldx, T, w, dscales, dx != nullptr, s);
     return CQ_OK;
 }
 

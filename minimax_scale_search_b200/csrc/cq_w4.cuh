@@ -8,6 +8,7 @@
 
 #include <atomic>
 #include <cstdint>
+#include <utility>
 
 #include "cq.h"
 
@@ -231,6 +232,38 @@ cudaError_t allow_shared(int bytes)
 inline cq_status launched()
 {
     return cudaGetLastError() == cudaSuccess ? CQ_OK : CQ_ERR_CUDA;
+}
+
+// Launches of one call that follow each other on a stream.  The first says early on that the next may begin; that
+// one is launched by launch_next, may run beside the first's last CTAs, and calls wait_for_previous before it touches
+// what the first wrote, or before its end where it touches none of it.  It never ends before the first has, so what
+// comes after it on the stream comes after both; the first is an ordinary launch, so what came before is done.
+// Saves the launch and what a wave's last CTAs leave idle: both gradients of 777 x 1,032 x 2,176 in 22.7 us for 24.7,
+// of 4,096 x 14,336 x 4,096 in 769 for 778; a table's gradient of 16 tokens in 8.3 us for 12.
+__device__ __forceinline__ void let_next_begin()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+__device__ __forceinline__ void wait_for_previous()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+template <class... P, class... A>
+cq_status launch_next(void (*kernel)(P...), unsigned ctas, int threads, int bytes, cudaStream_t stream, A &&...args)
+{
+    cudaLaunchConfig_t config = {};
+    config.gridDim = dim3(ctas);
+    config.blockDim = dim3(threads);
+    config.dynamicSmemBytes = bytes;
+    config.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    config.attrs = attr;
+    config.numAttrs = 1;
+    return cudaLaunchKernelEx(&config, kernel, std::forward<A>(args)...) == cudaSuccess ? CQ_OK : CQ_ERR_CUDA;
 }
 
 // A [T][n] operand of 16-bit values: 16-byte rows.

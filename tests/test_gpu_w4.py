@@ -582,3 +582,61 @@ def test_concurrent_calls_on_two_streams():
     for run in got:
         for a, b in zip(run, refs):
             assert all(torch.equal(i, j) for i, j in zip(a, b))
+
+
+@pytest.mark.parametrize("T,R,K", [(777, 1032, 2176), (40, 4096, 256), (2000, 136, 128)])
+def test_gradients_in_a_row_over_the_same_buffers(T, R, K):
+    """The launches of a call may overlap each other, but nothing before or after the call: inputs are
+    written right before it and cleared right after it, with nothing waited for."""
+    import torch
+    from minimax_scale_search_b200 import cq
+    rng = np.random.default_rng(T)
+    w, _, _ = make_layer(R, K, T)
+    inputs = [(values(rng, (T, R), "bf16")[0], values(rng, (T, K), "bf16")[0]) for _ in range(6)]
+    want = []
+    for dz, x in inputs:
+        want.append(cq.w4_linear_backward(dz, x, w))
+        torch.cuda.synchronize()
+    dz, x, dx = torch.empty_like(inputs[0][0]), torch.empty_like(inputs[0][1]), torch.empty_like(inputs[0][1])
+    ds = torch.empty_like(want[0][1])
+    got = []
+    torch.cuda.synchronize()
+    for a, b in inputs:
+        dz.copy_(a)
+        x.copy_(b)
+        cq.w4_linear_backward(dz, x, w, dx=dx, dscales=ds)
+        dz.zero_()
+        x.zero_()
+        got.append((dx.clone(), ds.clone()))
+        dx.fill_(-1)
+        ds.fill_(-1)
+    for (a, b), (c, d) in zip(got, want):
+        assert torch.equal(a, c) and torch.equal(b, d)
+
+
+@pytest.mark.parametrize("T,V,K", [(5, 40, 256), (1001, 300, 1152), (9000, 50, 384)])
+def test_table_gradients_in_a_row_over_the_same_buffers(T, V, K):
+    import torch
+    from minimax_scale_search_b200 import cq
+    rng = np.random.default_rng(T)
+    codes = device(rng.integers(0, 2 ** 32, (V * (K // 128), 16), dtype=np.uint32))
+    inputs = [(values(rng, (T, K), "bf16")[0], device(rng.integers(0, V, T))) for _ in range(6)]
+    want = []
+    for dout, ids in inputs:
+        want.append(cq.w4_embedding_backward(dout, ids, codes))
+        torch.cuda.synchronize()
+    dout, ids, out = torch.empty_like(inputs[0][0]), torch.empty_like(inputs[0][1]), torch.empty_like(want[0])
+    ws = torch.empty(cq.w4_embedding_workspace_bytes(T, K), dtype=torch.uint8, device="cuda")
+    got = []
+    torch.cuda.synchronize()
+    for a, b in inputs:
+        dout.copy_(a)
+        ids.copy_(b)
+        cq.w4_embedding_backward(dout, ids, codes, out=out, workspace=ws)
+        dout.zero_()
+        ids.zero_()
+        ws.zero_()
+        got.append(out.clone())
+        out.fill_(-1)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
