@@ -707,6 +707,8 @@ def w4_linear_backward(dz, x, w: W4Weights, *, want_dx: bool = True, want_dscale
         elif (dscales.shape != (K // GROUP, R) or dscales.dtype != torch.float32 or dscales.device != dz.device or
               not dscales.is_contiguous() or dscales.data_ptr() % 16):
             raise ValueError(f"dscales must be contiguous 16-byte aligned float32 [{K // GROUP}, {R}]")
+        elif any(_overlap(dscales, t) for t in (dz, x, dx, w.qweight, w.qzeros, w.scales) if t is not None):
+            raise ValueError("dscales must not overlap another operand")
     _call(context, lib.cq_w4_linear_backward, dz.data_ptr(), lddz, None if x is None else x.data_ptr(), ldx, dt, T,
           *w._arguments(), None if dx is None else dx.data_ptr(), lddx, None if dscales is None else dscales.data_ptr(), handle)
     return dx, dscales
@@ -821,8 +823,12 @@ def w4_embedding_backward(dout, ids, codes, *, multiplier: float = 1.0, stream=N
         out = _empty(context, (V, K // GROUP), ids, torch.float32)
     elif out.shape != (V, K // GROUP) or out.dtype != torch.float32 or out.device != ids.device or not out.is_contiguous():
         raise ValueError(f"out must be contiguous float32 [{V}, {K // GROUP}]")
+    elif _overlap(out, dout) or _overlap(out, ids) or _overlap(out, codes):
+        raise ValueError("out must not overlap another operand")
     if workspace is None:
         workspace = _empty(context, (wsb,), ids, torch.uint8)
+    elif any(_overlap(workspace, t) for t in (dout, ids, codes, out)):
+        raise ValueError("workspace must not overlap another operand")
     _call(context, lib.cq_w4_embedding_backward, dout.data_ptr(), dt, ids.data_ptr(), int(ids.dtype is torch.int64), T,
           codes.data_ptr(), V, K, multiplier, out.data_ptr(), workspace.data_ptr(), wsb, handle)
     return out

@@ -640,3 +640,25 @@ def test_table_gradients_in_a_row_over_the_same_buffers(T, V, K):
         out.fill_(-1)
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+def test_gradients_that_overlap_their_operands_are_refused():
+    import torch
+    from minimax_scale_search_b200 import cq
+    w, _, _ = make_layer(256, 256, 1)
+    buf = torch.zeros(64 * 256, dtype=torch.float16, device="cuda")
+    x, dz = buf[:8 * 256].view(8, 256), torch.zeros((8, 256), dtype=torch.float16, device="cuda")
+    spare = buf[2048:2048 + 1024].view(torch.float32).view(2, 256)
+    cq.w4_linear_backward(dz, x, w, dscales=spare)  # right behind x
+    with pytest.raises(ValueError, match="dscales must not overlap"):
+        cq.w4_linear_backward(dz, x, w, dscales=buf[2040:2040 + 1024].view(torch.float32).view(2, 256))
+    with pytest.raises(ValueError, match="dscales must not overlap"):
+        cq.w4_linear_backward(dz, dz, w, dx=buf[512:512 + 2048].view(8, 256), dscales=spare)
+    codes = torch.zeros((40 * 2, 16), dtype=torch.int32, device="cuda")
+    ids = torch.zeros(8, dtype=torch.int64, device="cuda")
+    dout = torch.zeros((8, 256), dtype=torch.float32, device="cuda")
+    with pytest.raises(ValueError, match="out must not overlap"):
+        cq.w4_embedding_backward(dout, ids, codes, out=dout.view(-1)[:80].view(40, 2))
+    with pytest.raises(ValueError, match="workspace must not overlap"):
+        cq.w4_embedding_backward(dout, ids, torch.zeros_like(codes), workspace=dout)
+    cq.w4_status()
