@@ -943,12 +943,15 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 }
 
 // dz = dy act'(pre) and its column sums.  A cluster of 8 CTAs owns 64 columns; its
-// 256 row slots take every 256th row, a thread 8 adjacent columns (16-byte accesses; two rows at a time were slower,
-// 86 us for 76).  The sums meet in shared memory and through distributed shared memory, in a fixed order.
-// Bound by HBM: 6 bytes per element, 4.66 TB/s at 4,096 x 14,336 silu, 3.6 gelu.
+// 256 row slots take every 256th row, a thread 8 adjacent columns (16-byte accesses).  A thread's operands come through
+// its own places in shared memory, kActAhead rows ahead: bytes in flight are what the rate hangs on, and in registers two rows
+// at a time cost more warps than they bring (86 us; one at a time 76; 71, 65, 64 with 2, 3, 4 ahead).  The sums meet
+// in shared memory and through distributed shared memory, in a fixed order.
+// Bound by HBM: 6 bytes per element, 5.5 TB/s (0.86 of the copy's rate) at 4,096 x 14,336 silu and relu, 4.4 gelu (its arithmetic).
 constexpr int kActCluster = 8;
 constexpr int kActThreads = 256;
-constexpr int kActColumns = 64;    // pieces of 128 bytes of a row (76 us for 4,096 x 14,336 silu; 256 bytes 79 us)
+constexpr int kActColumns = 64;    // pieces of 128 bytes of a row (256 bytes: silu 62 us for 64, gelu 83 for 79)
+constexpr int kActAhead = 4;
 
 template <class D>
 __global__ void __cluster_dims__(kActCluster, 1, 1) __launch_bounds__(kActThreads)
@@ -963,12 +966,27 @@ __global__ void __cluster_dims__(kActCluster, 1, 1) __launch_bounds__(kActThread
     const int64_t col0 = static_cast<int64_t>(blockIdx.x / kActCluster) * kActColumns;
     const int lane = threadIdx.x % kLanes, slot = threadIdx.x / kLanes;
     const int64_t col = col0 + 8 * lane;
+    __shared__ uint4 ring[kActAhead][2][kActThreads];
     float acc[8] = {};
     if (col < R) {
-        for (int64_t t = rank * kSlots + slot; t < T; t += kActCluster * kSlots) {
+        constexpr int kStep = kActCluster * kSlots;
+        auto fetch = [&](int64_t t, int i) {
+            if (t < T) {
+                tc::copy_async<16>(tc::smem_address(&ring[i][0][threadIdx.x]), dy + t * lddy + col, true);
+                tc::copy_async<16>(tc::smem_address(&ring[i][1][threadIdx.x]), pre + t * ldpre + col, true);
+            }
+            tc::copy_async_commit();
+        };
+        const int64_t first = rank * kSlots + slot;
+#pragma unroll
+        for (int i = 0; i < kActAhead; i++)
+            fetch(first + i * kStep, i);
+        int at = 0;
+        for (int64_t t = first; t < T; t += kStep) {
             float d[8], z[8];
-            widen<D>(*reinterpret_cast<const uint4 *>(dy + t * lddy + col), d);
-            widen<D>(*reinterpret_cast<const uint4 *>(pre + t * ldpre + col), z);
+            tc::copy_async_wait_but<kActAhead - 1>();
+            widen<D>(ring[at][0][threadIdx.x], d);
+            widen<D>(ring[at][1][threadIdx.x], z);
             slopes(z, act);
 #pragma unroll
             for (int j = 0; j < 8; j++) {
@@ -976,7 +994,10 @@ __global__ void __cluster_dims__(kActCluster, 1, 1) __launch_bounds__(kActThread
                 acc[j] += z[j];
             }
             *reinterpret_cast<uint4 *>(dz + t * lddz + col) = narrow<D>(z);
+            fetch(t + kActAhead * kStep, at);  // behind the store, which hangs on what the slot held
+            at = at + 1 < kActAhead ? at + 1 : 0;
         }
+        tc::copy_async_wait();
     }
     if (!dbias)
         return;  // the whole cluster

@@ -144,6 +144,18 @@ __device__ __forceinline__ void copy_async_arrive(uint32_t bar)
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
+__device__ __forceinline__ void copy_async_commit()
+{
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+// Waits for this thread's copies but those of its last kGroups commits.
+template <int kGroups>
+__device__ __forceinline__ void copy_async_wait_but()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(kGroups) : "memory");
+}
+
 __device__ __forceinline__ void copy_async_wait()
 {
     asm volatile("cp.async.wait_all;" ::: "memory");

@@ -662,3 +662,17 @@ def test_gradients_that_overlap_their_operands_are_refused():
     with pytest.raises(ValueError, match="workspace must not overlap"):
         cq.w4_embedding_backward(dout, ids, torch.zeros_like(codes), workspace=dout)
     cq.w4_status()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_activation_gradient_in_place_over_many_rows(dt):
+    """Rows are read ahead of those that are written: dz over dy or pre gives the same."""
+    import torch
+    from minimax_scale_search_b200 import cq
+    rng = np.random.default_rng(8)
+    dy, pre = values(rng, (5003, 136), dt, pad=8)[0], values(rng, (5003, 136), dt, 2.0, pad=8)[0]
+    want, db = cq.activation_backward(dy, pre, "silu")
+    for which in (0, 1):
+        a = [torch.cat([t, t[:, :8]], 1)[:, :136] for t in (dy, pre)]
+        got, b = cq.activation_backward(*a, "silu", out=a[which])
+        assert got is a[which] and torch.equal(got, want) and torch.equal(b, db)
