@@ -627,13 +627,29 @@ def _check_same_device(w, t):
         raise ValueError("the weights are on another device than the activations")
 
 
+def _extent(t):
+    """(address, rows, bytes from row to row, bytes of a row) of a contiguous tensor or one of contiguous rows."""
+    e = t.element_size()
+    if t.is_contiguous():
+        return t.data_ptr(), 1, 0, t.numel() * e
+    return t.data_ptr(), t.shape[0], t.stride(0) * e, t.shape[1] * e
+
+
 def _overlap(a, b):
-    """Whether two operands' memory may overlap."""
+    """Whether two operands share a byte: columns beside each other in one buffer do not."""
     if a.numel() == 0 or b.numel() == 0:
         return False
-    span = lambda t: sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1  # noqa: E731
-    a0, b0 = a.data_ptr(), b.data_ptr()
-    return a0 < b0 + span(b) * b.element_size() and b0 < a0 + span(a) * a.element_size()
+    (a0, ra, sa, wa), (b0, rb, sb, wb) = _extent(a), _extent(b)
+    if a0 >= b0 + (rb - 1) * sb + wb or b0 >= a0 + (ra - 1) * sa + wa:
+        return False
+    if ra > 1 and rb > 1 and sa != sb:  # row by row of the one with fewer of them
+        if ra > rb:
+            (a0, ra, sa, wa), (b0, rb, sb, wb) = (b0, rb, sb, wb), (a0, ra, sa, wa)
+        starts, ra, s = range(a0, a0 + ra * sa, sa), 1, sb
+    else:
+        starts, s = (a0,), sa or sb or 1
+    # the m for which wa bytes at `start` and wb bytes at b0 + m s meet: b's row number less a's
+    return any(max(1 - ra, (start - b0 - wb) // s + 1) <= min(rb - 1, (start - b0 + wa - 1) // s) for start in starts)
 
 
 def w4_linear(x, w: W4Weights, *, bias=None, activation: str = "none", residual=None, want_pre: bool = False,

@@ -1,0 +1,103 @@
+"""Which operands' memory may overlap, on the CPU: the binding's own check against the sets
+of bytes that two operands have, and each operator's refusals, with the launch
+itself replaced (host tensors that say they are CUDA tensors)."""
+import itertools
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def cq():
+    from minimax_scale_search_b200 import build
+    build.build()
+    from minimax_scale_search_b200 import cq as binding
+    return binding
+
+
+def bytes_of(t):
+    at = torch.zeros(t.shape, dtype=torch.int64)
+    for d, (n, s) in enumerate(zip(t.shape, t.stride())):
+        at += (torch.arange(n) * s).view([-1 if i == d else 1 for i in range(t.dim())])
+    at = t.data_ptr() + at.reshape(-1) * t.element_size()
+    return set((at[:, None] + torch.arange(t.element_size())).reshape(-1).tolist())
+
+
+def test_overlap_is_that_of_the_bytes(cq):
+    """Slices of one buffer: whole, by columns, by rows, every other row, of one row, of other widths and types."""
+    buf = torch.zeros(40 * 24, dtype=torch.float16)
+    wide, narrow = buf.view(40, 24), buf[8:8 + 44 * 16].view(44, 16)
+    views = [buf, buf[100:100], buf[:100], buf[90:200], buf[23:24], wide[3:9], wide[8:20], wide[20:21],
+             buf[:480].view(torch.float32), buf[480:520].view(torch.float32), narrow[::3, :8], narrow[1::3, 8:], narrow[5:6, 3:9]]
+    views += [wide[r0:r1:step, c0:c1] for r0, r1 in ((0, 40), (0, 4), (4, 8), (5, 6)) for step in (1, 2, 3)
+              for c0, c1 in ((0, 8), (8, 24), (4, 12), (0, 24), (23, 24))]
+    views += [buf[16 + k:16 + k + 30 * 24].view(30, 24)[:, :w] for k in (0, 8, 16, 23) for w in (1, 8, 9, 16)]  # rows that wrap around
+    sets = [bytes_of(v) for v in views]
+    for (a, sa), (b, sb) in itertools.product(zip(views, sets), repeat=2):
+        assert cq._overlap(a, b) == bool(sa & sb), (a.shape, a.stride(), a.storage_offset(), b.shape, b.stride(), b.storage_offset())
+
+
+# ---- the operators -----------------------------------------------------------------------------------
+
+
+class Cuda(torch.Tensor):
+    """A host tensor that the binding takes for a CUDA tensor."""
+    is_cuda = property(lambda self: True)
+
+
+def cuda(t):
+    return t.as_subclass(Cuda)
+
+
+R, K, T, V = 256, 256, 8, 40
+
+
+class Job:
+    """The operands of every operator, each in memory of its own, and a list of the launches made."""
+
+    def __init__(self, cq):
+        self.cq, self.made = cq, []
+        half = lambda *s: cuda(torch.zeros(s, dtype=torch.float16))  # noqa: E731
+        word = lambda *s: cuda(torch.zeros(s, dtype=torch.int32))  # noqa: E731
+        self.w = cq.W4Weights(word(K // 8, R), word(K // 128, R // 8), half(K // 128, R), R, K)
+        self.x, self.y, self.pre, self.res, self.dz, self.bias = half(T, K), half(T, R), half(T, R), half(T, R), half(T, R), half(R)
+        self.ids, self.codes, self.scales = cuda(torch.zeros(T, dtype=torch.int64)), word(V * K // 128, 16), half(V * K // 128)
+        self.dout, self.rows = half(T, K), half(T, K)
+        self.ws = cuda(torch.zeros(cq.w4_embedding_workspace_bytes(T, K), dtype=torch.uint8))
+
+    def linear(self, **kw):
+        return self.cq.w4_linear(self.x, self.w, **kw)
+
+    def backward(self, **kw):
+        return self.cq.w4_linear_backward(self.dz, self.x, self.w, **kw)
+
+    def activation(self, **kw):
+        return self.cq.activation_backward(self.dz, self.pre, "silu", **kw)
+
+    def lookup(self, **kw):
+        return self.cq.w4_embedding(self.ids, self.scales, self.codes, K, **kw)
+
+    def table(self, **kw):
+        return self.cq.w4_embedding_backward(self.dout, self.ids, self.codes, **kw)
+
+
+@pytest.fixture
+def job(cq, monkeypatch):
+    job = Job(cq)
+    monkeypatch.setattr(cq, "_place", lambda dev, stream: (0, None))
+    monkeypatch.setattr(cq, "_call", lambda context, function, *args: job.made.append(function))
+    return job
+
+
+def test_halves_of_one_buffer_are_taken(job):
+    """Columns of one buffer, side by side, share no memory: every operator takes them."""
+    cq = job.cq
+    buf = cuda(torch.zeros((T, 4 * R), dtype=torch.float16))
+    a, b, c, d = (buf[:, i * R:(i + 1) * R] for i in range(4))
+    cq.w4_linear(a, job.w, residual=b, want_pre=True, pre=c, out=d)
+    cq.w4_linear(a, job.w, residual=b, out=b)
+    cq.w4_linear_backward(a, b, job.w, dx=c)
+    cq.activation_backward(a, b, "gelu", out=c)
+    rows = cuda(torch.zeros((2 * T, K), dtype=torch.float16))
+    cq.w4_linear(rows[::2], job.w, out=rows[1::2])  # every other row
+    assert len(job.made) == 5
