@@ -652,6 +652,13 @@ def _overlap(a, b):
     return any(max(1 - ra, (start - b0 - wb) // s + 1) <= min(rb - 1, (start - b0 + wa - 1) // s) for start in starts)
 
 
+def _apart(name, output, **operands):
+    """Refuses an output whose memory overlaps an operand's."""
+    for other, t in operands.items():
+        if t is not None and _overlap(output, t):
+            raise ValueError(f"{name} must not overlap {other}")
+
+
 def w4_linear(x, w: W4Weights, *, bias=None, activation: str = "none", residual=None, want_pre: bool = False,
               stream=None, out=None, pre=None):
     """y = activation(x W^T + bias) + residual, W the layer's 4-bit weights.
@@ -674,8 +681,7 @@ def w4_linear(x, w: W4Weights, *, bias=None, activation: str = "none", residual=
         out, ldy = _empty(context, (T, R), x), R
     else:
         ldy = _rows16("out", out, T, R, x)
-        if _overlap(out, x):
-            raise ValueError("out must not overlap x")
+        _apart("out", out, x=x, bias=bias, qweight=w.qweight, qzeros=w.qzeros, scales=w.scales)
         if residual is not None and _overlap(out, residual) and (out.data_ptr() != residual.data_ptr() or ldy != ldres):
             raise ValueError("out must be the residual itself, or not overlap it")
     ldpre = 0
@@ -684,8 +690,7 @@ def w4_linear(x, w: W4Weights, *, bias=None, activation: str = "none", residual=
             pre, ldpre = _empty(context, (T, R), x), R
         else:
             ldpre = _rows16("pre", pre, T, R, x)
-            if _overlap(pre, x) or _overlap(pre, out) or (residual is not None and _overlap(pre, residual)):
-                raise ValueError("pre must not overlap another operand")
+            _apart("pre", pre, x=x, out=out, residual=residual, bias=bias, qweight=w.qweight, qzeros=w.qzeros, scales=w.scales)
     elif pre is not None:
         raise ValueError("pre is written only with want_pre")
     _call(context, lib.cq_w4_linear, x.data_ptr(), ldx, dt, T, *w._arguments(), None if bias is None else bias.data_ptr(), act,

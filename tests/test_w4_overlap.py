@@ -89,6 +89,30 @@ def job(cq, monkeypatch):
     return job
 
 
+def over(t, shape, dtype, tail=False):
+    """An operand of this shape and type over the first (or last) bytes of t."""
+    words = t.reshape(-1).view(torch.uint8)
+    n = torch.zeros(shape, dtype=dtype).numel() * torch.empty(0, dtype=dtype).element_size()
+    return words[words.numel() - n if tail else 0:][:n].view(dtype).view(shape)
+
+
+HALF = torch.float16
+
+
+def big(n):
+    return cuda(torch.zeros(n, dtype=HALF))
+
+
+def refused(job, call, name, target, others):
+    """`call(**{name: memory})` is refused where that memory has the first or the last bytes of an operand."""
+    for other in others:
+        for tail in (False, True):
+            memory = over(other, *target, tail=tail)
+            with pytest.raises(ValueError, match="overlap"):
+                call(**{name: memory})
+    assert not job.made
+
+
 def test_halves_of_one_buffer_are_taken(job):
     """Columns of one buffer, side by side, share no memory: every operator takes them."""
     cq = job.cq
@@ -101,3 +125,24 @@ def test_halves_of_one_buffer_are_taken(job):
     rows = cuda(torch.zeros((2 * T, K), dtype=torch.float16))
     cq.w4_linear(rows[::2], job.w, out=rows[1::2])  # every other row
     assert len(job.made) == 5
+
+
+def test_layer_refuses_an_output_over_any_operand(job):
+    job.w = job.cq.W4Weights(over(big(64 * R), (K // 8, R), torch.int32), job.w.qzeros, job.w.scales, R, K)
+    words = job.w.qweight
+    refused(job, job.linear, "out", ((T, R), HALF), [job.x, words])
+    refused(job, lambda **kw: job.linear(want_pre=True, **kw), "pre", ((T, R), HALF), [job.x, words])
+    # the smaller operands lie within the output's memory
+    for small in ("bias", "qzeros", "scales"):
+        for name in ("out", "pre"):
+            memory = big(T * R).view(T, R)
+            flat, w, bias = memory.view(-1), job.w, None
+            if small == "bias":
+                bias = flat[512:512 + R]
+            elif small == "qzeros":
+                w = job.cq.W4Weights(w.qweight, over(flat, (K // 128, R // 8), torch.int32, tail=True), w.scales, R, K)
+            else:
+                w = job.cq.W4Weights(w.qweight, w.qzeros, over(flat, (K // 128, R), HALF, tail=True), R, K)
+            with pytest.raises(ValueError, match="overlap"):
+                job.cq.w4_linear(job.x, w, bias=bias, want_pre=name == "pre", **{name: memory})
+    assert not job.made
