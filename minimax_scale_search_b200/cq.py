@@ -717,8 +717,7 @@ def w4_linear_backward(dz, x, w: W4Weights, *, want_dx: bool = True, want_dscale
         dx, lddx = _empty(context, (T, K), dz), K
     else:
         lddx = _rows16("dx", dx, T, K, dz)
-        if _overlap(dx, dz) or (want_dscales and _overlap(dx, x)):
-            raise ValueError("dx must not overlap dz or x")
+        _apart("dx", dx, dz=dz, x=x if want_dscales else None, qweight=w.qweight, qzeros=w.qzeros, scales=w.scales)
     if not want_dscales:
         x = dscales = None
     else:
@@ -728,8 +727,8 @@ def w4_linear_backward(dz, x, w: W4Weights, *, want_dx: bool = True, want_dscale
         elif (dscales.shape != (K // GROUP, R) or dscales.dtype != torch.float32 or dscales.device != dz.device or
               not dscales.is_contiguous() or dscales.data_ptr() % 16):
             raise ValueError(f"dscales must be contiguous 16-byte aligned float32 [{K // GROUP}, {R}]")
-        elif any(_overlap(dscales, t) for t in (dz, x, dx, w.qweight, w.qzeros, w.scales) if t is not None):
-            raise ValueError("dscales must not overlap another operand")
+        else:
+            _apart("dscales", dscales, dz=dz, x=x, dx=dx, qweight=w.qweight, qzeros=w.qzeros, scales=w.scales)
     _call(context, lib.cq_w4_linear_backward, dz.data_ptr(), lddz, None if x is None else x.data_ptr(), ldx, dt, T,
           *w._arguments(), None if dx is None else dx.data_ptr(), lddx, None if dscales is None else dscales.data_ptr(), handle)
     return dx, dscales

@@ -146,3 +146,16 @@ def test_layer_refuses_an_output_over_any_operand(job):
             with pytest.raises(ValueError, match="overlap"):
                 job.cq.w4_linear(job.x, w, bias=bias, want_pre=name == "pre", **{name: memory})
     assert not job.made
+
+
+def test_layer_gradients_refuse_outputs_over_any_operand(job):
+    refused(job, job.backward, "dx", ((T, K), HALF), [job.dz, job.x, job.w.qweight])
+    refused(job, lambda **kw: job.backward(want_dscales=False, **kw), "dx", ((T, K), HALF), [job.dz, job.w.qweight])
+    for small in ("qzeros", "scales"):
+        memory = big(T * K).view(T, K)
+        zeros = over(memory, (K // 128, R // 8), torch.int32) if small == "qzeros" else job.w.qzeros
+        scales = over(memory, (K // 128, R), HALF) if small == "scales" else job.w.scales
+        with pytest.raises(ValueError, match="overlap"):
+            job.cq.w4_linear_backward(job.dz, None, job.cq.W4Weights(job.w.qweight, zeros, scales, R, K), want_dscales=False, dx=memory)
+    refused(job, job.backward, "dscales", ((K // 128, R), torch.float32), [job.dz, job.x, job.w.qweight])
+    assert not job.made
