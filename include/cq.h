@@ -266,7 +266,7 @@ cq_status cq_w4_linear_backward(const void *dz, int64_t lddz, const void *x, int
 
 /* dz = dy * act'(pre), rounded to dtype, and dbias[r] = sum_t of it before the rounding (fp32 [R], nullable,
  * 4-byte aligned; written, not added to).  relu' is 1 where pre > 0, else 0; CQ_ACT_NONE copies dy.  All [T][R], R % 8 == 0; dz
- * may be dy itself or pre itself (with the same ld). */
+ * may be dy itself or pre itself (with the same ld); dbias must not overlap the others. */
 cq_status cq_activation_backward(const void *dy, int64_t lddy, const void *pre, int64_t ldpre, int dtype, int64_t T,
                                  int64_t R, int activation, void *dz, int64_t lddz, float *dbias, void *stream);
 

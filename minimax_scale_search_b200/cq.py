@@ -759,6 +759,8 @@ def activation_backward(dy, pre, activation: str, *, want_dbias: bool = True, st
         dbias = _empty(context, (R,), dy, torch.float32)
     elif dbias.shape != (R,) or dbias.dtype != torch.float32 or dbias.device != dy.device or not dbias.is_contiguous():
         raise ValueError(f"dbias must be contiguous float32 [{R}]")
+    else:
+        _apart("dbias", dbias, dy=dy, pre=pre, out=out)
     _call(context, lib.cq_activation_backward, dy.data_ptr(), lddy, pre.data_ptr(), ldpre, dt, T, R, act, out.data_ptr(),
           lddz, None if dbias is None else dbias.data_ptr(), handle)
     return out, dbias

@@ -159,3 +159,11 @@ def test_layer_gradients_refuse_outputs_over_any_operand(job):
             job.cq.w4_linear_backward(job.dz, None, job.cq.W4Weights(job.w.qweight, zeros, scales, R, K), want_dscales=False, dx=memory)
     refused(job, job.backward, "dscales", ((K // 128, R), torch.float32), [job.dz, job.x, job.w.qweight])
     assert not job.made
+
+
+def test_activation_gradient_refuses_a_bias_gradient_over_any_operand(job):
+    refused(job, job.activation, "dbias", ((R,), torch.float32), [job.dz, job.pre])
+    refused(job, lambda **kw: job.activation(out=job.y, **kw), "dbias", ((R,), torch.float32), [job.y])
+    job.activation(out=job.dz)
+    job.activation(out=job.pre)
+    assert len(job.made) == 2
