@@ -279,7 +279,7 @@ cq_status cq_w4_status(void *stream);
 /* Rows of a quantised table, from the selection's own scales [V*K/128] and codes [V*K/128][16] of a [V][K] matrix:
  * out[t][i] = multiplier * (scale * q) of row ids[t], each product in fp32, rounded once to dtype (CQ_DTYPE_FP32 too);
  * an id outside [0, V) gives a row of zeros.  ids are int32 (ids64 == 0) or int64 (ids64 == 1), out is [T][K]
- * contiguous and 16-byte aligned, codes 4-byte aligned. */
+ * contiguous and 16-byte aligned, codes 4-byte aligned.  out must not overlap an input. */
 cq_status cq_w4_embedding(const void *ids, int ids64, int64_t T, const uint16_t *scales, const uint32_t *codes,
                           int64_t V, int64_t K, float multiplier, int dtype, void *out, void *stream);
 

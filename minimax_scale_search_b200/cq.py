@@ -813,6 +813,8 @@ def w4_embedding(ids, scales, codes, K: int, *, multiplier: float = 1.0, dtype=N
         out = _empty(context, shape, ids, dtype)
     elif out.shape != shape or out.dtype != dtype or out.device != ids.device or not out.is_contiguous():
         raise ValueError(f"out must be contiguous {dtype} {list(shape)}")
+    else:
+        _apart("out", out, ids=ids, scales=scales, codes=codes)
     _call(context, lib.cq_w4_embedding, ids.data_ptr(), int(ids.dtype is torch.int64), T, scales.data_ptr(), codes.data_ptr(),
           V, K, multiplier, dt, out.data_ptr(), handle)
     return out
@@ -845,12 +847,12 @@ def w4_embedding_backward(dout, ids, codes, *, multiplier: float = 1.0, stream=N
         out = _empty(context, (V, K // GROUP), ids, torch.float32)
     elif out.shape != (V, K // GROUP) or out.dtype != torch.float32 or out.device != ids.device or not out.is_contiguous():
         raise ValueError(f"out must be contiguous float32 [{V}, {K // GROUP}]")
-    elif _overlap(out, dout) or _overlap(out, ids) or _overlap(out, codes):
-        raise ValueError("out must not overlap another operand")
+    else:
+        _apart("out", out, dout=dout, ids=ids, codes=codes)
     if workspace is None:
         workspace = _empty(context, (wsb,), ids, torch.uint8)
-    elif any(_overlap(workspace, t) for t in (dout, ids, codes, out)):
-        raise ValueError("workspace must not overlap another operand")
+    else:
+        _apart("workspace", workspace, dout=dout, ids=ids, codes=codes, out=out)
     _call(context, lib.cq_w4_embedding_backward, dout.data_ptr(), dt, ids.data_ptr(), int(ids.dtype is torch.int64), T,
           codes.data_ptr(), V, K, multiplier, out.data_ptr(), workspace.data_ptr(), wsb, handle)
     return out

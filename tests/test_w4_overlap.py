@@ -167,3 +167,25 @@ def test_activation_gradient_refuses_a_bias_gradient_over_any_operand(job):
     job.activation(out=job.dz)
     job.activation(out=job.pre)
     assert len(job.made) == 2
+
+
+def test_lookup_refuses_an_output_over_any_operand(job):
+    refused(job, job.lookup, "out", ((T, K), HALF), [job.codes])
+    for small in ("ids", "scales"):
+        memory = big(T * K).view(T, K)
+        for tail in (False, True):
+            ids = over(memory, (T,), torch.int64, tail) if small == "ids" else job.ids
+            scales = over(memory, (V * K // 128,), HALF, tail) if small == "scales" else job.scales
+            with pytest.raises(ValueError, match="overlap"):
+                job.cq.w4_embedding(ids, scales, job.codes, K, out=memory)
+    assert not job.made
+    job.lookup(out=job.rows)
+    assert len(job.made) == 1
+
+
+def test_table_gradient_refuses_outputs_over_any_operand(job):
+    refused(job, job.table, "out", ((V, K // 128), torch.float32), [job.dout, job.codes])
+    refused(job, lambda **kw: job.table(workspace=job.ws, **kw), "out", ((V, K // 128), torch.float32), [job.ws])
+    assert not job.made
+    job.table(out=cuda(torch.zeros((V, K // 128))), workspace=job.ws)
+    assert len(job.made) == 1
