@@ -107,8 +107,16 @@ __device__ __forceinline__ float normal_distribution(float z, float &phi)
     return z < 0.0f ? tail : 1.0f - tail;
 }
 
-// act(z) for a result that is rounded to 16 bits: exp and the quotient to a few units of
-// 2^-22, far inside that rounding.  The quotients' limits hold: exp(-z) = inf gives 0.
+// 1 / (1 + exp(-a)), its small values to their own last digits: only exp(-|a|) is taken, so that the divisor lies between
+// 1 and 2 (the fast quotient gives 0 for divisors above 2^126, where bf16 still has normal results).
+__device__ __forceinline__ float sigmoid(float a)
+{
+    const float e = __expf(-fabsf(a)), p = __fdividef(1.0f, 1.0f + e);
+    return a < 0.0f ? e * p : p;
+}
+
+// act(z) for a result that is rounded to 16 bits.  exp(x) of the fast instruction is within (2 + 1.2 |x|) 2^-23 of
+// its value and x within 5 roundings: 2^-15 at most, where exp(x) is about to leave fp32, and 2^-20 for |x| < 2.
 template <int n>
 __device__ __forceinline__ void activate(float (&z)[n], int act)
 {
@@ -125,15 +133,15 @@ __device__ __forceinline__ void activate(float (&z)[n], int act)
     } else if (act == CQ_ACT_GELU_TANH) {  // z/2 (1 + tanh u) = z / (1 + exp(-2u))
 #pragma unroll
         for (int i = 0; i < n; i++)
-            z[i] = __fdividef(z[i], 1.0f + __expf(-1.5957691216057308f * (z[i] + 0.044715f * z[i] * z[i] * z[i])));
+            z[i] *= sigmoid(1.5957691216057308f * (z[i] + 0.044715f * z[i] * z[i] * z[i]));
     } else if (act == CQ_ACT_SILU) {
 #pragma unroll
         for (int i = 0; i < n; i++)
-            z[i] = __fdividef(z[i], 1.0f + __expf(-z[i]));
+            z[i] *= sigmoid(z[i]);
     }
 }
 
-// act'(z), to a few units of 2^-22 of its terms.
+// act'(z), each of its terms as far off as that.
 template <int n>
 __device__ __forceinline__ void slopes(float (&z)[n], int act)
 {
@@ -152,13 +160,13 @@ __device__ __forceinline__ void slopes(float (&z)[n], int act)
     } else if (act == CQ_ACT_GELU_TANH) {  // p = (1 + tanh u) / 2 = 1 / (1 + exp(-2u)), 1 - tanh^2 u = 4 p (1 - p)
 #pragma unroll
         for (int i = 0; i < n; i++) {
-            const float q = z[i] * z[i], p = __fdividef(1.0f, 1.0f + __expf(-2.0f * kC * z[i] * (1.0f + 0.044715f * q)));
+            const float q = z[i] * z[i], p = sigmoid(2.0f * kC * z[i] * (1.0f + 0.044715f * q));
             z[i] = p + z[i] * (2.0f * p * (1.0f - p)) * (kC * (1.0f + 0.134145f * q));
         }
     } else if (act == CQ_ACT_SILU) {
 #pragma unroll
         for (int i = 0; i < n; i++) {
-            const float p = __fdividef(1.0f, 1.0f + __expf(-z[i]));
+            const float p = sigmoid(z[i]);
             z[i] = p * (1.0f + z[i] * (1.0f - p));
         }
     } else {

@@ -1,0 +1,111 @@
+"""The operators on 4-bit weights at the ends of their types' ranges: every finite
+16-bit argument of the activations and of their slopes.
+
+The fp32 arithmetic behind a result of 16 bits is counted as follows, u = 2^-24 a rounding:
+exp(x) by the fast instruction is within (2 + 1.173 |x|) 2^-23 of its value (the CUDA guide's bound), its
+argument's own roundings, five at most, add 5 |x| u; a quotient with a divisor between 1 and 2 adds 2^-22, the
+ratio of Mills 2^-22 and its evaluation 2^-21 (eight steps, terms of at most twice the result), the few products after them 2^-22.  Values below
+2^-126 carry 2^-149 of absolute error, times factors of at most 300."""
+import math
+
+import numpy as np
+import pytest
+
+from minimax_scale_search_b200 import synth  # noqa: F401  (the package, before any GPU work)
+
+pytestmark = pytest.mark.gpu
+
+U = {"bf16": 2.0 ** -8, "fp16": 2.0 ** -11}
+TINY = {"bf16": 2.0 ** -134 + 2.0 ** -140, "fp16": 2.0 ** -25}
+ACTIVATIONS = ("none", "relu", "gelu", "gelu_tanh", "silu")
+C = math.sqrt(2 / math.pi)
+
+
+def every_finite(dt):
+    """[T, 128] of every finite value of the type, T = 510 or 496."""
+    import torch
+    bits = np.arange(1 << 16, dtype=np.uint16)
+    x = torch.from_numpy(bits.view(np.int16)).view({"bf16": torch.bfloat16, "fp16": torch.float16}[dt])
+    return x[torch.isfinite(x.float())].view(-1, 128).cuda()
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def sigmoid(a):
+    """(p, 1 - p), each to its own last digits."""
+    e = np.exp(-np.minimum(np.abs(a), 1000.0))
+    big, small = 1 / (1 + e), e / (1 + e)
+    return np.where(a < 0, small, big), np.where(a < 0, big, small)
+
+
+def parts(z, act):
+    """The argument of the activation's exponential, the activation, and the two terms of its slope."""
+    if act == "none":
+        return 0 * z, z, 0 * z + 1, 0 * z
+    if act == "relu":
+        return 0 * z, np.maximum(z, 0), (z > 0).astype(np.float64), 0 * z
+    if act == "gelu":
+        p = 0.5 * np.vectorize(math.erfc, otypes=[np.float64])(-z / math.sqrt(2))
+        a = -np.minimum(z * z / 2, 1000.0)
+        return a, z * p, p, z * np.exp(a) / math.sqrt(2 * math.pi)
+    a = z if act == "silu" else 2 * C * (z + 0.044715 * z ** 3)
+    p, q = sigmoid(a)
+    return a, z * p, p, z * p * q * (1.0 if act == "silu" else 2 * C * (1 + 3 * 0.044715 * z * z))
+
+
+def arithmetic(a):
+    """Relative error of the fp32 arithmetic around exp(a); beyond 110 the exponential has left fp32."""
+    a = np.minimum(np.abs(a), 110.0)
+    return (2 + 1.173 * a) * 2.0 ** -23 + 5 * a * 2.0 ** -24 + 2.0 ** -20
+
+
+def identity():
+    """A layer of 128 x 128 whose weights are 1 on the diagonal and 0 beside it."""
+    import torch
+    from minimax_scale_search_b200 import cq
+    u = np.full((128, 128), 8, dtype=np.uint32)
+    np.fill_diagonal(u, 9)
+    words = np.zeros((16, 128), dtype=np.uint32)
+    for j in range(8):
+        words |= u[:, j::8].T << np.uint32(4 * j)
+    return cq.w4_weights(cq.GPTQTensors(torch.from_numpy(words.view(np.int32)).cuda(),
+                                        torch.full((1, 16), 0x77777777, dtype=torch.int32, device="cuda"),
+                                        torch.ones((1, 128), dtype=torch.float16, device="cuda"),
+                                        torch.zeros(128, dtype=torch.int32, device="cuda")))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("act", ACTIVATIONS)
+@pytest.mark.parametrize("rows", [8, 510])
+def test_activation_of_every_finite_value(act, dt, rows):
+    """Through the few-row kernel and through the tensor-core kernel; small results of large negative arguments keep
+    their digits down to the type's smallest."""
+    from minimax_scale_search_b200 import cq
+    import torch
+    x, w = every_finite(dt), identity()
+    got = [cq.w4_linear(x[i:i + rows], w, activation=act, want_pre=True) for i in range(0, x.shape[0], rows)]
+    y, pre = (torch.cat([g[k] for g in got]) for k in (0, 1))
+    z = f64(x)
+    assert np.array_equal(f64(pre), z)  # one product with 1 and 127 with 0
+    a, e, _, _ = parts(z, act)
+    assert np.all(np.abs(f64(y) - e) <= (U[dt] + arithmetic(a)) * np.abs(e) + TINY[dt])
+
+
+def check_slopes(act, dt, keep):
+    import torch
+    from minimax_scale_search_b200 import cq
+    pre = torch.where(keep(every_finite(dt)), every_finite(dt), 0)
+    dz, db = cq.activation_backward(torch.ones_like(pre), pre, act)
+    a, _, p, q = parts(f64(pre), act)
+    off = arithmetic(a) * (np.abs(p) + np.abs(q))  # before the result's rounding
+    assert np.all(np.abs(f64(dz) - (p + q)) <= U[dt] * np.abs(p + q) + off + TINY[dt])
+    sums = (pre.shape[0] + 8) * 2.0 ** -24 * np.abs(p + q).sum(0)
+    assert np.all(np.abs(f64(db) - (p + q).sum(0)) <= off.sum(0) + sums + pre.shape[0] * 2.0 ** -140)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("act", ACTIVATIONS)
+def test_slope_of_every_value_up_to_1e19(act, dt):
+    check_slopes(act, dt, lambda z: z.float().abs() <= 1e19)
