@@ -160,7 +160,8 @@ __device__ __forceinline__ void slopes(float (&z)[n], int act)
     } else if (act == CQ_ACT_GELU_TANH) {  // p = (1 + tanh u) / 2 = 1 / (1 + exp(-2u)), 1 - tanh^2 u = 4 p (1 - p)
 #pragma unroll
         for (int i = 0; i < n; i++) {
-            const float q = z[i] * z[i], p = sigmoid(2.0f * kC * z[i] * (1.0f + 0.044715f * q));
+            const float q = fminf(z[i] * z[i], 1e6f);  // p is 0 or 1 long before; inf would meet its 1 - p = 0
+            const float p = sigmoid(2.0f * kC * z[i] * (1.0f + 0.044715f * q));
             z[i] = p + z[i] * (2.0f * p * (1.0f - p)) * (kC * (1.0f + 0.134145f * q));
         }
     } else if (act == CQ_ACT_SILU) {

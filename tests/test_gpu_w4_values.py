@@ -109,3 +109,25 @@ def check_slopes(act, dt, keep):
 @pytest.mark.parametrize("act", ACTIVATIONS)
 def test_slope_of_every_value_up_to_1e19(act, dt):
     check_slopes(act, dt, lambda z: z.float().abs() <= 1e19)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("act", ACTIVATIONS)
+def test_slope_of_every_finite_value(act, dt):
+    """Beyond 1.8e19 the argument's square leaves fp32; the slope there is 0 or 1."""
+    check_slopes(act, dt, lambda z: z == z)
+
+
+@pytest.mark.parametrize("act", ACTIVATIONS)
+def test_slope_of_what_is_not_finite(act):
+    """inf and NaN as the formulas have them: relu's slope is a comparison, the others multiply."""
+    import torch
+    from minimax_scale_search_b200 import cq
+    z = torch.tensor([[math.nan, math.inf, -math.inf, 0.0] * 2], dtype=torch.bfloat16, device="cuda")
+    got = cq.activation_backward(torch.ones_like(z), z, act)[0][0, :3].float().tolist()
+    if act == "none":
+        assert got == [1, 1, 1]
+    elif act == "relu":
+        assert got == [0, 1, 0]
+    else:
+        assert all(math.isnan(v) for v in got)
