@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
 // 64 outputs a warp.  A thread reads 4 adjacent outputs' words at once; a word is 8 inputs, whose pairs
 // (q, q + 4) come out of it with a shift and a mask.  That order of the inputs is as good as any for the
 // m16n8k16 product if the activations' pairs are the same.  The codes enter as integers, zero point
-// taken off, and each group's fp32 sum is scaled after, so the weights are exact.  The sets' and the
+// taken off (with bf16 times 2^-11, made good at the end), and each group's fp32 sum is scaled after, so the weights are exact.  The sets' and the
 // cluster's sums meet in shared memory in a fixed order.
 //
 // Measured: 30,336 x 16,384 in 68 us for 1 to 8 rows (3.8 TB/s, 0.59 of HBM), 93 us for 13 (fp16); 14,336 x 4,096 in 12.4 us.
@@ -657,7 +657,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 const uint32_t z = reinterpret_cast<const uint32_t *>(at + kFewWords + 256)[8 * half + 4 * m + quad / 2] >> (16 * (quad & 1));
 #pragma unroll
                 for (int k = 0; k < 4; k++)
-                    zero[m][k] = zero_pair<D>((z >> (4 * k)) & 15u);
+                    zero[m][k] = code_zero_pair<D>((z >> (4 * k)) & 15u);
             }
 #pragma unroll
             for (int j = 0; j < 4; j++) {
@@ -761,6 +761,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             z[0] += parts[k];
         if (r >= w.R)
             continue;
+        z[0] *= D::kCodeUnit;
         z[0] += ep.bias ? D::to_float(ep.bias[r]) : 0.0f;
         if (ep.pre)
             ep.pre[t * ep.ldpre + r] = D::from_float(z[0]);
@@ -847,7 +848,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                     const int64_t g = g0 + i;
                     if (g >= w.K / kGroup)
                         continue;
-                    const uint32_t zero = zero_pair<FP16>(inside ? (w.qzeros[(g * w.R + r) / 8] >> (4 * (r & 7))) & 15u : 0u);
+                    const uint32_t zero = code_zero_pair<FP16>(inside ? (w.qzeros[(g * w.R + r) / 8] >> (4 * (r & 7))) & 15u : 0u);
                     float part = 0.0f;
                     for (int c = 0; c < kGroup; c += 32) {
                         uint32_t word[4], v[32];

@@ -28,15 +28,20 @@ constexpr uint32_t kLow = 0x000F000Fu;
 struct BF16 {
     using pair = __nv_bfloat162;
     static constexpr uint32_t kMagic = 0x43004300u;  // 128
+    // Codes that enter products as integers do so times 2^-11 (mantissas of 2^-4), so that 128 inputs of any size times
+    // codes of up to 16 stay in fp32 where the scale brings the result back into it; the smallest input times 2^-11
+    // is an fp32 value still.
+    static constexpr uint32_t kCodeMagic = 0x3D803D80u;
+    static constexpr float kCodeUnit = 2048.0f;
     static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b)
     {
         const pair d = __hsub2(reinterpret_cast<const pair &>(a), reinterpret_cast<const pair &>(b));
         return reinterpret_cast<const uint32_t &>(d);
     }
-    // u - z - 1 of codes q and q + 4 of a word; zero as zero_pair gives it, low is kLow.
+    // (u - z - 1) / kCodeUnit of codes q and q + 4 of a word; zero as code_zero_pair gives it, low is kLow.
     static __device__ __forceinline__ uint32_t code_pair(uint32_t word, int q, uint32_t zero, uint32_t low)
     {
-        return sub(((word >> (4 * q)) & low) | kMagic, zero);
+        return sub(((word >> (4 * q)) & low) | kCodeMagic, zero);
     }
     static __device__ __forceinline__ float to_float(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
     static __device__ __forceinline__ uint16_t from_float(float f) { return __bfloat16_as_ushort(__float2bfloat16_rn(f)); }
@@ -50,12 +55,14 @@ struct BF16 {
 struct FP16 {
     using pair = __half2;
     static constexpr uint32_t kMagic = 0x64006400u;  // 1024
+    static constexpr uint32_t kCodeMagic = kMagic;   // 128 inputs below 2^16 times 16 are below 2^27
+    static constexpr float kCodeUnit = 1.0f;
     static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b)
     {
         const pair d = __hsub2(reinterpret_cast<const pair &>(a), reinterpret_cast<const pair &>(b));
         return reinterpret_cast<const uint32_t &>(d);
     }
-    // u - z - 1 of codes q and q + 4 of a word; zero as zero_pair gives it, low is kLow.  Ten mantissa bits hold an
+    // u - z - 1 of codes q and q + 4 of a word; zero as code_zero_pair gives it, low is kLow.  Ten mantissa bits hold an
     // odd code where it stands, as 1024 + 16 u; a sixteenth of that less 64 + z + 1 is exact, and a shift is saved.
     static __device__ __forceinline__ uint32_t code_pair(uint32_t word, int q, uint32_t zero, uint32_t low)
     {
@@ -81,6 +88,13 @@ template <class T>
 __device__ __forceinline__ uint32_t zero_pair(uint32_t nibble)
 {
     return T::kMagic + (nibble + 1u) * 0x00010001u;
+}
+
+// The same for code_pair().
+template <class T>
+__device__ __forceinline__ uint32_t code_zero_pair(uint32_t nibble)
+{
+    return T::kCodeMagic + (nibble + 1u) * 0x00010001u;
 }
 
 __device__ __forceinline__ float half_bits(uint16_t b)

@@ -131,3 +131,39 @@ def test_slope_of_what_is_not_finite(act):
         assert got == [0, 1, 0]
     else:
         assert all(math.isnan(v) for v in got)
+
+
+def layer_of(u, scale, R=8, K=256):
+    """A layer whose every code is u with a zero point of 8 (weights scale * (u - 8)), its scales all `scale`."""
+    import torch
+    from minimax_scale_search_b200 import cq
+    word = int(np.array([u * 0x11111111], dtype=np.uint32).view(np.int32)[0])
+    full = lambda *s, v: torch.full(s, v, dtype=torch.int32, device="cuda")  # noqa: E731
+    return cq.w4_weights(cq.GPTQTensors(full(K // 8, R, v=word), full(K // 128, R // 8, v=0x77777777),
+                                        torch.full((K // 128, R), scale, dtype=torch.float16, device="cuda"),
+                                        torch.arange(K, dtype=torch.int32, device="cuda") // 128))
+
+
+@pytest.mark.parametrize("T", [1, 13, 40])
+def test_large_inputs_with_small_scales(T):
+    """Inputs whose sums with the integer codes alone would leave fp32 (128 x 7 x 2^120), where the result does not."""
+    import torch
+    from minimax_scale_search_b200 import cq
+    x = torch.full((T, 256), 2.0 ** 120, dtype=torch.bfloat16, device="cuda")
+    x[:, 1::2] *= 0.75
+    got = f64(cq.w4_linear(x, layer_of(15, 2.0 ** -14)))
+    assert np.all(got == 256 * 7 * 0.875 * 2.0 ** 120 * 2.0 ** -14)  # 7 x 7 x 2^k: exact
+
+
+@pytest.mark.parametrize("T", [1, 13, 40])
+@pytest.mark.parametrize("power", [-126, -130, -133])
+def test_smallest_inputs(T, power):
+    """Inputs down to bfloat16's smallest value keep their digits: each sum below is 7 x 2^k, a bfloat16 value."""
+    import torch
+    from minimax_scale_search_b200 import cq
+    x = torch.full((T, 256), 2.0 ** power, dtype=torch.bfloat16, device="cuda")
+    got = f64(cq.w4_linear(x, layer_of(15, 1.0)))
+    assert np.all(got == 256 * 7 * 2.0 ** power)
+    one = torch.zeros_like(x)
+    one[:, 37] = 2.0 ** power
+    assert np.all(f64(cq.w4_linear(one, layer_of(15, 1.0))) == 7 * 2.0 ** power)
