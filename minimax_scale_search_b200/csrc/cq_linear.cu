@@ -118,7 +118,7 @@ struct Unpack<FP16> {
 };
 
 // bf16: s = hi + lo, hi the scale rounded to 8 bits and lo the at most 3 bits left, so
-// n lo is exact and fma(n, hi, n lo) rounds n s once.
+// n lo is exact and fma(n, hi, n lo) rounds n s once.  An infinite scale is hi alone: inf - inf leaves no rest.
 template <>
 struct Unpack<BF16> {
     uint32_t zero;
@@ -128,7 +128,7 @@ struct Unpack<BF16> {
         const float s = half_bits(scale);
         const __nv_bfloat16 h = __float2bfloat16_rn(s);
         hi = __bfloat162bfloat162(h);
-        lo = __bfloat162bfloat162(__float2bfloat16_rn(s - __bfloat162float(h)));
+        lo = __bfloat162bfloat162(__float2bfloat16_rn((scale & 0x7C00u) == 0x7C00u ? 0.0f : s - __bfloat162float(h)));
     }
     __device__ __forceinline__ uint4 operator()(uint32_t w, uint32_t low) const
     {

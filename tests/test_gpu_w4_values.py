@@ -167,3 +167,24 @@ def test_smallest_inputs(T, power):
     one = torch.zeros_like(x)
     one[:, 37] = 2.0 ** power
     assert np.all(f64(cq.w4_linear(one, layer_of(15, 1.0))) == 7 * 2.0 ** power)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("T", [1, 13, 40])
+def test_infinite_and_missing_scales(T, dt):
+    """Infinite weights of one sign times positive inputs are infinite, not NaN; a scale of NaN is NaN; neither
+    leaves its output (layer) or its group's inputs (input gradient)."""
+    import torch
+    from minimax_scale_search_b200 import cq
+    torch_dt = {"bf16": torch.bfloat16, "fp16": torch.float16}[dt]
+    w = layer_of(9, 0.5, R=16, K=384)
+    w.scales[1, 3], w.scales[1, 5], w.scales[2, 8] = math.inf, -math.inf, math.nan
+    y = cq.w4_linear(torch.ones((T, 384), dtype=torch_dt, device="cuda"), w).float()
+    expect = torch.full((T, 16), 192.0, device="cuda")
+    expect[:, 3], expect[:, 5], expect[:, 8] = math.inf, -math.inf, math.nan
+    assert torch.equal(y.nan_to_num(7.0), expect.nan_to_num(7.0))
+    dz = torch.ones((T, 16), dtype=torch_dt, device="cuda")
+    dz[:, 5] = 2.0
+    w.scales[1, 5] = 0.5
+    dx = cq.w4_linear_backward(dz, None, w, want_dscales=False)[0].float()
+    assert bool((dx[:, :128] == 8.5).all() and torch.isposinf(dx[:, 128:256]).all() and torch.isnan(dx[:, 256:]).all())
