@@ -230,7 +230,8 @@ cq_status cq_gptq_dequantize(const int32_t *qweight, const int32_t *qzeros, cons
  * A matrix operand [T][n] of 16-bit values has rows of n consecutive elements, ld
  * elements apart: 16-byte aligned, ld % 8 == 0, ld >= n.  qweight is 16-byte aligned and
  * scales 16-byte aligned.  dtype is CQ_DTYPE_BF16 or CQ_DTYPE_FP16.  T >= 0 rows (T == 0:
- * nothing to do, except that summed gradients become zero); R % 8 == 0, K % 128 == 0, K > 0.
+ * nothing to do, except that summed gradients become zero); R % 8 == 0, K % 128 == 0, K > 0; T and K below 2^31, R at
+ * most 2^31 - 128.
  * Sums are fp32 (fp64 where stated) in a fixed order; every result is rounded once to its
  * type.  Non-finite values propagate as IEEE arithmetic has them, within their own row of T
  * (a product with a zero weight or zero input of the same row included). */

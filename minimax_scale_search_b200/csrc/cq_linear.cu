@@ -1030,7 +1030,7 @@ cq_status check_layer(int64_t T, int dtype, int64_t R, int64_t K, const void *qw
     if (T < 0 || R < 0 || K <= 0 || R % 8 != 0 || K % kGroup != 0 || (dtype != CQ_DTYPE_BF16 && dtype != CQ_DTYPE_FP16))
         return CQ_ERR_INVALID_ARG;
     constexpr int64_t kMost = static_cast<int64_t>(1) << 31;
-    if (T >= kMost || R >= kMost || K >= kMost)
+    if (T >= kMost || R > kMost - kM || K >= kMost)  // the last tile of outputs ends in 31 bits too
         return CQ_ERR_UNSUPPORTED;
     if (R > 0 && (!qweight || !qzeros || !scales || !is_aligned(qweight, 16) || !is_aligned(qzeros, 4) ||
                   !is_aligned(scales, 16)))
