@@ -709,26 +709,30 @@ def w4_linear_backward(dz, x, w: W4Weights, *, want_dx: bool = True, want_dscale
     _check_same_device(w, dz)
     T, R, K = dz.shape[0], w.R, w.K
     lddz = _rows16("dz", dz, T, R, dz)
-    handle, context = _place(dz.device, stream)
     ldx = lddx = 0
+    if not want_dscales:
+        x = dscales = None
+    elif x is None:
+        raise ValueError("dscales needs x")
+    else:
+        ldx = _rows16("x", x, T, K, dz)
+    handle, context = _place(dz.device, stream)
     if not want_dx:
         dx = None
     elif dx is None:
         dx, lddx = _empty(context, (T, K), dz), K
     else:
         lddx = _rows16("dx", dx, T, K, dz)
-        _apart("dx", dx, dz=dz, x=x if want_dscales else None, qweight=w.qweight, qzeros=w.qzeros, scales=w.scales)
+        _apart("dx", dx, dz=dz, x=x, qweight=w.qweight, qzeros=w.qzeros, scales=w.scales)
     if not want_dscales:
-        x = dscales = None
+        pass
+    elif dscales is None:
+        dscales = _empty(context, (K // GROUP, R), dz, torch.float32)
+    elif (dscales.shape != (K // GROUP, R) or dscales.dtype != torch.float32 or dscales.device != dz.device or
+          not dscales.is_contiguous() or dscales.data_ptr() % 16):
+        raise ValueError(f"dscales must be contiguous 16-byte aligned float32 [{K // GROUP}, {R}]")
     else:
-        ldx = _rows16("x", x, T, K, dz)
-        if dscales is None:
-            dscales = _empty(context, (K // GROUP, R), dz, torch.float32)
-        elif (dscales.shape != (K // GROUP, R) or dscales.dtype != torch.float32 or dscales.device != dz.device or
-              not dscales.is_contiguous() or dscales.data_ptr() % 16):
-            raise ValueError(f"dscales must be contiguous 16-byte aligned float32 [{K // GROUP}, {R}]")
-        else:
-            _apart("dscales", dscales, dz=dz, x=x, dx=dx, qweight=w.qweight, qzeros=w.qzeros, scales=w.scales)
+        _apart("dscales", dscales, dz=dz, x=x, dx=dx, qweight=w.qweight, qzeros=w.qzeros, scales=w.scales)
     _call(context, lib.cq_w4_linear_backward, dz.data_ptr(), lddz, None if x is None else x.data_ptr(), ldx, dt, T,
           *w._arguments(), None if dx is None else dx.data_ptr(), lddx, None if dscales is None else dscales.data_ptr(), handle)
     return dx, dscales

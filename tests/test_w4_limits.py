@@ -23,3 +23,21 @@ def test_outputs_whose_last_tile_passes_31_bits_are_refused(cq, R):
         cq.CQ_ERR_UNSUPPORTED
     assert cq.lib.cq_w4_linear(FAKE, 128, 0, 40, FAKE, FAKE, FAKE, R, 128, NONE, 0, NONE, 0, FAKE, R, NONE, 0, NONE) == \
         cq.CQ_ERR_UNSUPPORTED
+
+
+class Cuda(torch.Tensor):
+    """A host tensor that the binding takes for a CUDA tensor."""
+    is_cuda = property(lambda self: True)
+
+
+def test_scale_gradient_asks_for_the_input(cq, monkeypatch):
+    monkeypatch.setattr(cq, "_place", lambda dev, stream: (0, None))
+    monkeypatch.setattr(cq, "_call", lambda *a: pytest.fail("launched"))
+    made = lambda *s, dtype=torch.float16: torch.zeros(s, dtype=dtype).as_subclass(Cuda)  # noqa: E731
+    w = cq.W4Weights(made(32, 64, dtype=torch.int32), made(2, 8, dtype=torch.int32), made(2, 64), 64, 256)
+    dz = made(4, 64)
+    for kw in ({}, dict(want_dx=False), dict(dx=made(4, 256))):
+        with pytest.raises(ValueError, match="dscales needs x"):
+            cq.w4_linear_backward(dz, None, w, **kw)
+        with pytest.raises(ValueError, match=r"x must be \[4, 256\]"):
+            cq.w4_linear_backward(dz, made(4, 128), w, **kw)
