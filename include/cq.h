@@ -273,7 +273,7 @@ cq_status cq_activation_backward(const void *dy, int64_t lddy, const void *pre, 
 
 /* The layer's and its gradients' kernels hand work from warp to warp through bounded waits.  A wait that has not ended
  * after four seconds gives up: the kernel then returns, its outputs unfinished.  This call synchronises `stream` and
- * returns CQ_ERR_CUDA when that has happened on the current device since the library was loaded (or when the stream
+ * returns CQ_ERR_CUDA when that has happened on the current device since it was last called (or when the stream
  * reports an error), else CQ_OK. */
 cq_status cq_w4_status(void *stream);
 

@@ -79,8 +79,6 @@ struct Stages {
     static_assert(kRaw % kUnpackSets == 0, "phases");
 };
 
-__device__ int g_gave_up;  // set when a wait in a kernel ran out; read by cq_w4_status
-
 // Eight codes of a word as 16-bit values s (u - z - 1), in order, each rounded once.
 template <class D>
 struct Unpack;
@@ -462,10 +460,7 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
         tc::copy_async_wait();
     }
     __syncthreads();
-    if (*stop) {
-        tc::let_copies_land();
-        g_gave_up = 1;
-    }
+    tc::report(stop);
     if (warp == kIssueWarp)
         tc::tmem_free(tmem, S::kColumns);
     if (ranks == 1)
@@ -720,10 +715,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         }
     }
     __syncthreads();  // every copy has landed and been read: the ring becomes the sets' sums
-    if (*stop) {
-        tc::let_copies_land();
-        g_gave_up = 1;
-    }
+    tc::report(stop);
     float *sums = reinterpret_cast<float *>(shared), *cta_sums = sums + kFewSets * 8 * NT * kM;
     if (warp < 2 * kFewSets) {
 #pragma unroll
@@ -934,10 +926,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         }
     }
     __syncthreads();
-    if (*stop) {
-        tc::let_copies_land();
-        g_gave_up = 1;
-    }
+    tc::report(stop);
     if (warp == 5)
         tc::tmem_free(tmem, 2 * kGradN);
     wait_for_previous();  // the input gradient before it: the two share inputs only
@@ -1244,8 +1233,8 @@ cq_status cq_w4_status(void *stream)
 {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return CQ_ERR_CUDA;
-    int gave_up = 0;
-    if (cudaMemcpyFromSymbol(&gave_up, g_gave_up, sizeof(gave_up)) != cudaSuccess)
+    bool gave_up = false;
+    if (tc::take_report(&gave_up) != cudaSuccess)
         return CQ_ERR_CUDA;
     return gave_up ? CQ_ERR_CUDA : CQ_OK;
 }

@@ -74,7 +74,7 @@ __device__ __forceinline__ uint64_t now()
 
 // Waits for a phase; false when it did not come, or when another thread of the CTA has
 // given up (*stop).  Every role then leaves its loop.
-__device__ __forceinline__ bool barrier_wait(uint32_t bar, uint32_t parity, volatile int *stop)
+__device__ __forceinline__ bool barrier_wait(uint32_t bar, uint32_t parity, volatile int *stop, uint64_t most = kMostNanoseconds)
 {
     if (barrier_try(bar, parity))
         return true;
@@ -85,7 +85,7 @@ __device__ __forceinline__ bool barrier_wait(uint32_t bar, uint32_t parity, vola
         if (i % 64 == 0) {
             if (*stop)
                 return false;
-            if (now() - start > kMostNanoseconds) {
+            if (now() - start > most) {
                 *stop = 1;
                 return false;
             }
@@ -94,9 +94,9 @@ __device__ __forceinline__ bool barrier_wait(uint32_t bar, uint32_t parity, vola
 }
 
 // The same for a whole warp, with one answer for its lanes.
-__device__ __forceinline__ bool barrier_wait_warp(uint32_t bar, uint32_t parity, volatile int *stop)
+__device__ __forceinline__ bool barrier_wait_warp(uint32_t bar, uint32_t parity, volatile int *stop, uint64_t most = kMostNanoseconds)
 {
-    return __all_sync(0xFFFFFFFFu, barrier_wait(bar, parity, stop));
+    return __all_sync(0xFFFFFFFFu, barrier_wait(bar, parity, stop, most));
 }
 
 // Two of them at once.
@@ -113,6 +113,30 @@ __device__ __forceinline__ void let_copies_land()
 {
     for (int i = 0; i < 1000; i++)
         __nanosleep(1000);
+}
+
+static __device__ int g_gave_up;  // set when a wait in a kernel of this file ran out
+
+// By every thread of a CTA whose roles have left their loops.
+__device__ __forceinline__ void report(volatile int *stop)
+{
+    if (*stop) {
+        let_copies_land();
+        g_gave_up = 1;
+    }
+}
+
+// Whether a wait has run out on the current device since this was last asked.
+static cudaError_t take_report(bool *gave_up)
+{
+    int set = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&set, g_gave_up, sizeof(set));
+    *gave_up = set != 0;
+    if (e == cudaSuccess && set) {
+        set = 0;
+        e = cudaMemcpyToSymbol(g_gave_up, &set, sizeof(set));
+    }
+    return e;
 }
 
 // ---- copies ----------------------------------------------------------------------------------------
