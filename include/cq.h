@@ -248,7 +248,7 @@ cq_status cq_gptq_dequantize(const int32_t *qweight, const int32_t *qzeros, cons
  * x is multiplied by W; up to CQ_W4_EXACT_ROWS rows with W's exact values (integers in the
  * products, the scale applied to each group's fp32 sum), above with W rounded to
  * dtype to nearest even (as cq_gptq_dequantize's fp16 output; with fp16 a weight beyond
- * 65504 is then infinite).  y and pre must not overlap each other or an input (but for y over the residual itself). */
+ * 65504 is then infinite, which the Python binding refuses).  y and pre must not overlap each other or an input (but for y over the residual itself). */
 #define CQ_W4_EXACT_ROWS 16
 cq_status cq_w4_linear(const void *x, int64_t ldx, int dtype, int64_t T, const int32_t *qweight,
                        const int32_t *qzeros, const uint16_t *gptq_scales, int64_t R, int64_t K, const void *bias,

@@ -508,6 +508,7 @@ def estimate_diagonals(X, row_offsets, *, dtype=None, stream=None, means=None, o
     return means, out
 
 
+EXACT_ROWS = 16  # rows of x up to which a layer multiplies by the weights' exact values
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
 
@@ -520,6 +521,7 @@ class W4Weights:
     scales: "object"   # torch.float16 [K/128, R]
     R: int
     K: int
+    beyond_fp16: bool = False  # some weight may lie beyond float16's range
 
     def _arguments(self):
         return self.qweight.data_ptr(), self.qzeros.data_ptr(), self.scales.data_ptr(), self.R, self.K
@@ -529,7 +531,10 @@ def w4_weights(t: GPTQTensors) -> W4Weights:
     """Checks GPTQ v1 tensors once, for w4_linear and w4_linear_backward: shapes,
     types, devices, and that g_idx is i // 128 (read to the host here; an
     act-order layer raises ValueError).  The result keeps the tensors and refers
-    to their memory: values written into them later are the layer's."""
+    to their memory: values written into them later are the layer's.  Where a scale
+    times a code's largest distance from its zero point passes 65504, float16 calls
+    whose product rounds the weights (more than EXACT_ROWS rows, and dx) raise
+    ValueError; that is found out here too, once."""
     import torch
     if t.qweight.dim() != 2:
         raise ValueError("qweight must be [K/8, R]")
@@ -546,7 +551,10 @@ def w4_weights(t: GPTQTensors) -> W4Weights:
         raise ValueError("the tensors must be CUDA tensors of one device")
     if not np.array_equal(t.g_idx.cpu().numpy(), np.arange(K) // GROUP):
         raise ValueError("g_idx must be i // 128: act-order layers are not supported here")
-    return W4Weights(t.qweight, t.qzeros, t.scales, R, K)
+    zero = (t.qzeros[:, :, None] >> torch.arange(0, 32, 4, dtype=torch.int32, device=t.qzeros.device)) & 15
+    most = torch.maximum(14 - zero, zero + 1).view(t.scales.shape) * t.scales.float().abs()
+    beyond = (most >= 65520.0) & most.isfinite()  # rounds to inf
+    return W4Weights(t.qweight, t.qzeros, t.scales, R, K, bool(beyond.any()))
 
 
 def _place(dev, stream):
@@ -635,6 +643,11 @@ def _extent(t):
     return t.data_ptr(), t.shape[0], t.stride(0) * e, t.shape[1] * e
 
 
+def _check_range(w, t):
+    if w.beyond_fp16 and _float_code(t.dtype) == DTYPE_FP16:
+        raise ValueError("the layer has weights beyond float16's range: call it with bfloat16")
+
+
 def _overlap(a, b):
     """Whether two operands share a byte: columns beside each other in one buffer do not."""
     if a.numel() == 0 or b.numel() == 0:
@@ -671,6 +684,8 @@ def w4_linear(x, w: W4Weights, *, bias=None, activation: str = "none", residual=
     dt, act = _dtype16("x", x), _activation(activation)
     _check_same_device(w, x)
     T, R, K = x.shape[0], w.R, w.K
+    if T > EXACT_ROWS:
+        _check_range(w, x)
     ldx = _rows16("x", x, T, K, x)
     if bias is not None and (bias.shape != (R,) or bias.dtype != x.dtype or bias.device != x.device or
                              not bias.is_contiguous() or bias.data_ptr() % 16):
@@ -710,6 +725,8 @@ def w4_linear_backward(dz, x, w: W4Weights, *, want_dx: bool = True, want_dscale
     T, R, K = dz.shape[0], w.R, w.K
     lddz = _rows16("dz", dz, T, R, dz)
     ldx = lddx = 0
+    if want_dx:
+        _check_range(w, dz)
     if not want_dscales:
         x = dscales = None
     elif x is None:
