@@ -527,6 +527,16 @@ class W4Weights:
         return self.qweight.data_ptr(), self.qzeros.data_ptr(), self.scales.data_ptr(), self.R, self.K
 
 
+def _beyond_fp16(t):
+    """Whether a scale times a code's largest distance from its zero point rounds to inf in float16."""
+    import torch
+    if t.scales.numel() == 0 or float(t.scales.abs().amax()) * 16 < 65520.0:
+        return False
+    zero = (t.qzeros[:, :, None] >> torch.arange(0, 32, 4, dtype=torch.int32, device=t.qzeros.device)) & 15
+    most = torch.maximum(14 - zero, zero + 1).view(t.scales.shape) * t.scales.float().abs()
+    return bool(((most >= 65520.0) & most.isfinite()).any())
+
+
 def w4_weights(t: GPTQTensors) -> W4Weights:
     """Checks GPTQ v1 tensors once, for w4_linear and w4_linear_backward: shapes,
     types, devices, and that g_idx is i // 128 (read to the host here; an
@@ -551,10 +561,7 @@ def w4_weights(t: GPTQTensors) -> W4Weights:
         raise ValueError("the tensors must be CUDA tensors of one device")
     if not np.array_equal(t.g_idx.cpu().numpy(), np.arange(K) // GROUP):
         raise ValueError("g_idx must be i // 128: act-order layers are not supported here")
-    zero = (t.qzeros[:, :, None] >> torch.arange(0, 32, 4, dtype=torch.int32, device=t.qzeros.device)) & 15
-    most = torch.maximum(14 - zero, zero + 1).view(t.scales.shape) * t.scales.float().abs()
-    beyond = (most >= 65520.0) & most.isfinite()  # rounds to inf
-    return W4Weights(t.qweight, t.qzeros, t.scales, R, K, bool(beyond.any()))
+    return W4Weights(t.qweight, t.qzeros, t.scales, R, K, _beyond_fp16(t))
 
 
 def _place(dev, stream):
