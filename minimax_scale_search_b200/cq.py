@@ -809,7 +809,8 @@ def _table(ids, codes, K):
         raise ValueError("ids must be a contiguous CUDA int32 or int64 tensor")
     if K <= 0 or K % GROUP:
         raise ValueError("K must be a positive multiple of 128")
-    if codes.element_size() != 4 or codes.device != ids.device or not codes.is_contiguous() or codes.numel() % (K // 8):
+    if codes.dtype not in (torch.int32, torch.uint32) or codes.device != ids.device or not codes.is_contiguous() or \
+            codes.numel() % (K // 8):
         raise ValueError("codes must hold contiguous 32-bit words of whole rows, on the device of ids")
     return ids.numel(), codes.numel() // (K // 8)
 
@@ -829,9 +830,9 @@ def w4_embedding(ids, scales, codes, K: int, *, multiplier: float = 1.0, dtype=N
     import torch
     K = int(K)
     T, V = _table(ids, codes, K)
-    if scales.element_size() != 2 or scales.numel() != V * (K // GROUP) or scales.device != ids.device or \
-            not scales.is_contiguous():
-        raise ValueError("scales must hold V*K/128 contiguous 16-bit patterns on the device of ids")
+    if scales.dtype not in (torch.int16, torch.uint16, torch.float16) or scales.numel() != V * (K // GROUP) or \
+            scales.device != ids.device or not scales.is_contiguous():
+        raise ValueError("scales must hold V*K/128 contiguous binary16 patterns on the device of ids")
     if dtype is None:
         dtype = torch.float16 if out is None else out.dtype
     dt = _float_type("dtype", dtype)

@@ -41,3 +41,24 @@ def test_scale_gradient_asks_for_the_input(cq, monkeypatch):
             cq.w4_linear_backward(dz, None, w, **kw)
         with pytest.raises(ValueError, match=r"x must be \[4, 256\]"):
             cq.w4_linear_backward(dz, made(4, 128), w, **kw)
+
+
+def test_table_of_other_types_is_refused(cq, monkeypatch):
+    """Patterns of binary16 and words of codes: bfloat16 scales or float codes would be read as something else."""
+    monkeypatch.setattr(cq, "_place", lambda dev, stream: (0, None))
+    made = []
+    monkeypatch.setattr(cq, "_call", lambda *a: made.append(a))
+    new = lambda *s, dtype: torch.zeros(s, dtype=dtype).as_subclass(Cuda)  # noqa: E731
+    ids, K, V = new(3, dtype=torch.int64), 256, 5
+    for scales in (torch.int16, torch.uint16, torch.float16):
+        for codes in (torch.int32, torch.uint32):
+            cq.w4_embedding(ids, new(V * 2, dtype=scales), new(V * 2, 16, dtype=codes), K)
+            cq.w4_embedding_backward(new(3, K, dtype=torch.float32), ids, new(V * 2, 16, dtype=codes))
+    assert len(made) == 12
+    with pytest.raises(ValueError, match="scales"):
+        cq.w4_embedding(ids, new(V * 2, dtype=torch.bfloat16), new(V * 2, 16, dtype=torch.int32), K)
+    with pytest.raises(ValueError, match="codes"):
+        cq.w4_embedding(ids, new(V * 2, dtype=torch.float16), new(V * 2, 16, dtype=torch.float32), K)
+    with pytest.raises(ValueError, match="codes"):
+        cq.w4_embedding_backward(new(3, K, dtype=torch.float32), ids, new(V * 2, 16, dtype=torch.float32))
+    assert len(made) == 12
