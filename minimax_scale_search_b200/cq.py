@@ -796,9 +796,13 @@ def activation_backward(dy, pre, activation: str, *, want_dbias: bool = True, st
 
 def w4_status(stream=None) -> int:
     """Synchronises ``stream`` and returns CQ_OK; raises CQError when a wait inside a
-    kernel of w4_linear or w4_linear_backward has given up on the current device since
+    kernel of w4_linear or w4_linear_backward has given up on the stream's device since
     this was last called (its outputs are then unfinished)."""
-    _check(lib.cq_w4_status(_stream_handle(stream)), "cq_w4_status")
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    with torch.cuda.device(stream.device):
+        _check(lib.cq_w4_status(_stream_handle(stream)), "cq_w4_status")
     return CQ_OK
 
 

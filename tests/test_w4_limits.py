@@ -62,3 +62,21 @@ def test_table_of_other_types_is_refused(cq, monkeypatch):
     with pytest.raises(ValueError, match="codes"):
         cq.w4_embedding_backward(new(3, K, dtype=torch.float32), ids, new(V * 2, 16, dtype=torch.float32))
     assert len(made) == 12
+
+
+def test_status_is_that_of_the_streams_device(cq, monkeypatch):
+    """The report lies on the device of the stream, which need not be the current one."""
+    import contextlib
+    from types import SimpleNamespace
+    current, asked = [0], []
+
+    @contextlib.contextmanager
+    def device(d):
+        before, current[0] = current[0], d
+        yield
+        current[0] = before
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(cq, "lib", SimpleNamespace(cq_w4_status=lambda s: asked.append((current[0], s.value)) or 0))
+    assert cq.w4_status(SimpleNamespace(device=3, cuda_stream=77)) == cq.CQ_OK
+    assert asked == [(3, 77)] and current == [0]
