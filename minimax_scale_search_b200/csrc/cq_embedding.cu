@@ -17,8 +17,8 @@
 //     lies inside a chunk is done, others leave a part at the chunk's head or tail;
 //  3. the runs across chunks, from their parts in order.
 // So a row that every token names is summed by many threads, and the order of the sums is fixed.
-// 8,192 bf16 tokens x 4,096: 33 us (26 the first launch, whose ranking takes 20 on its own and hides the pass over
-// dout); 65,536 x 1,024: 61 us, half of them the radix sort.  Each launch but a call's first begins before the one
+// 8,192 bf16 tokens x 4,096: 33 us (26 the first launch: its ranking takes 20 on its own, the pass over dout 13 at HBM's
+// rate, and they overlap in part); 65,536 x 1,024: 61 us, half of them the radix sort.  Each launch but a call's first begins before the one
 // in front of it has ended and waits for it where it needs its results (without: 73 us, 9,000 x 256 41 for 29).
 #include <type_traits>
 
@@ -29,8 +29,11 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kUnits = kThreads / kWordsPerGroup;       // units of a CTA at a time: kGroups groups of one token
-constexpr int kRankMost = 8192;                         // tokens sorted by counting,
-constexpr int64_t kRankRows = 1 << 24;                  // of tables whose row numbers fp32 holds
+// Tokens sorted by counting: what the 48 KB of a CTA's static shared memory hold, and up to there counting is the faster
+// (calls of width 1,024 by counting and by radix sort: 12 and 25 us at 1,024 tokens, 15 and 27 at 4,096, 25 and 30 at 8,192;
+// of width 4,096: 12 and 24, 21 and 34, 33 and 44);
+constexpr int kRankMost = 8192;
+constexpr int64_t kRankRows = 1 << 24;                  // and tables whose row numbers fp32 holds
 constexpr int kRankBlock = 32;                          // tokens ranked by a CTA, one a lane
 constexpr int kChunk = 8;                               // sorted tokens per partial sum
 constexpr int kSortTokens = 1024;                       // per CTA of the radix sort

@@ -44,10 +44,13 @@ struct Layer {
 // instructions, copies scales and zero points.  CTAs are persistent; two accumulators in tensor memory let
 // a tile's epilogue run under the next tile's products.  Where there are too few tiles for the SMs, a cluster shares
 // a tile's contraction and adds its sums up through distributed shared memory, in the order of its ranks.
+// The tensor core's fp32 sums are cut off, not rounded, at each step: 16,384 terms of one sign come out 3e-5 low, a
+// sixteenth of half a step of fp16, and nothing is done against it here (the scale gradient, whose results are fp32, has spans).
 //
-// Measured (bf16, events, one B200): 4,096 x 14,336 x 4,096 in 361 us, 1.33 PFLOP/s, 0.78 of the measured cuBLAS burst; 395 us
-// the input gradient.  Run for seconds the power limit holds it at 1.45 GHz: 438 us where cuBLAS, of weights already
-// unpacked, takes 393.  64 x 30,336 x 16,384: 130 us, 2.0 TB/s, bound by issue slots (305 of 500 cycles a stage: unpacking).
+// Measured (bf16, events, one B200): 4,096 x 14,336 x 4,096 in 355 us, 1.35 PFLOP/s, 0.80 of the measured cuBLAS burst; 390 us
+// the input gradient.  Run for seconds the power limit holds them at 1.36 and 1.43 GHz: 417 and 453 us, 680 and 720 cycles a stage of
+// 256 tokens, where cuBLAS, of weights already unpacked, takes 395 us at 1.24 GHz (the tensor core alone needs 512 cycles; 96 KB go
+// through shared memory).  64 x 30,336 x 16,384: 130 us, 2.0 TB/s, bound by issue slots (305 of 500 cycles a stage: unpacking).
 
 constexpr int kM = 128;
 constexpr int kChunk = 64;                     // contraction per stage
@@ -160,11 +163,6 @@ struct Ring {
             slot = 0;
             parity ^= 1;
         }
-    }
-    __device__ __forceinline__ void skip(int n)
-    {
-        for (int i = 0; i < n; i++)
-            next();
     }
 };
 
@@ -774,7 +772,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 // epilogue multiplies a lane's 128 sums of a group by its codes and adds them up, so dW stays in
 // tensor memory.  The tensor core's fp32 sums are cut off, not rounded, at each of its steps of 16 tokens;
 // kSpan bounds the drift: every span of 512 tokens has sums of its own, which the epilogue adds up (against 64 bits
-// 5e-7 off at 4,096 tokens; 1.1e-6 with spans of 1,024).  Measured: 4,096 x 14,336 x 4,096 in 380 us, 1.27 PFLOP/s.  Two accumulators, persistent CTAs; warps 0-3 epilogue, 4 copies, 5 issues.
+// 5e-7 off at 4,096 tokens; 1.1e-6 with spans of 1,024).  Measured: 4,096 x 14,336 x 4,096 in 383 us, 1.26 PFLOP/s, for seconds
+// 452 at 1.56 GHz.  Two accumulators, persistent CTAs; warps 0-3 epilogue, 4 copies, 5 issues.
 
 constexpr int kGradN = 256;
 constexpr int kGradB = kGradN * kChunk * 2;
@@ -937,7 +936,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 // its own places in shared memory, kActAhead rows ahead: bytes in flight are what the rate hangs on, and in registers two rows
 // at a time cost more warps than they bring (86 us; one at a time 76; 71, 65, 64 with 2, 3, 4 ahead).  The sums meet
 // in shared memory and through distributed shared memory, in a fixed order.
-// Bound by HBM: 6 bytes per element, 5.5 TB/s (0.86 of the copy's rate) at 4,096 x 14,336 silu and relu, 4.4 gelu (its arithmetic).
+// Bound by HBM: 6 bytes per element, 5.5 TB/s (0.86 of the copy's rate) at 4,096 x 14,336 silu and relu (64 us); by issue slots,
+// 85% of them used, gelu (80 us, 4.4 TB/s) and its tanh form (69 to 72 us).
 constexpr int kActCluster = 8;
 constexpr int kActThreads = 256;
 constexpr int kActColumns = 64;    // pieces of 128 bytes of a row (256 bytes: silu 62 us for 64, gelu 83 for 79)
@@ -1067,9 +1067,11 @@ cq_status run_product(const uint16_t *act, int64_t ld, int64_t T, const Layer &w
                            stream, act_map, word_map, w, T, ep);
 }
 
-// Tokens per tile and CTAs per tile: the least time by a count of waves.  A stage of N tokens costs 2 N cycles on the
-// tensor core but never less than about 400, what the chain of waits between the warps takes; a tile about 3,000 more to start
-// and to end, a cluster's sums 2,000 and a few for each token.
+// Tokens per tile and CTAs per tile: the least time by a count of waves.  A stage of N tokens counts 2 N cycles, what the
+// tensor core takes, but never less than about 400, what the chain of waits between the warps takes; a call about 3,000 more to start
+// and to end, a cluster's sums 2,000 and a few for each token.  It ranks the choices and is no forecast: a stage of 256 tokens
+// measures 680 to 820 cycles, and the results of a CTA's only tile, which nothing hides, are not in it (333 x 4,104 x 1,152:
+// 10,200 cycles by the rule, 14.5 us measured).  17 x 4,096 x 4,096 took 14.5 us in clusters of 4 where it took 22.5 without.
 template <class D, bool kGradient>
 cq_status product(const uint16_t *act, int64_t ld, int64_t T, const Layer &w, const Epilogue &ep, cudaStream_t stream)
 {

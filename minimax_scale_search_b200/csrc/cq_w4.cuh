@@ -103,8 +103,8 @@ __device__ __forceinline__ float half_bits(uint16_t b)
 }
 
 // Phi(z), the normal distribution function, and phi(z), its density: the tail beyond |z| is phi M(|z|), M the ratio of
-// Mills, here a polynomial of degree 8 in 1 / (1 + 0.3 |z|) (fitted for the least largest relative error on [0, 14], 1.3e-7), so that the
-// small values of large negative z keep their digits.  17 instructions, where erfc has three times as many.
+// Mills, here a polynomial of degree 8 in 1 / (1 + 0.3 |z|), fitted on [0, 14] and there within 2.1e-7 of it (4.8e-7 as evaluated in
+// fp32), so that the small values of large negative z keep their digits.  17 instructions, where erfc has three times as many.
 __device__ __forceinline__ float normal_distribution(float z, float &phi)
 {
     const float t = __fdividef(1.0f, fmaf(0.3f, fabsf(z), 1.0f));
