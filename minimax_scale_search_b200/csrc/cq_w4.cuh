@@ -130,7 +130,7 @@ __device__ __forceinline__ float sigmoid(float a)
 }
 
 // act(z) for a result that is rounded to 16 bits.  exp(x) of the fast instruction is within (2 + 1.2 |x|) 2^-23 of
-// its value and x within 5 roundings: 2^-15 at most, where exp(x) is about to leave fp32, and 2^-20 for |x| < 2.
+// its value and x within 5 roundings: 2^-14 in all where exp(x) is about to leave fp32, 2^-19 for |x| < 2.
 template <int n>
 __device__ __forceinline__ void activate(float (&z)[n], int act)
 {
